@@ -445,6 +445,129 @@ MOE_API moe_status moe_permute_rows(int32_t dtype, const void *src, const int32_
                                     void *dst, int64_t rows, int32_t d, moe_stream_t stream);
 
 /*
+ * Block-scaled e4m3: the experts' products on 8-bit values.
+ *
+ * A block of values is held as q = e4m3(x / s) and one fp32 scale s.
+ * Activations have blocks of 1 row x 128 columns, weights of 128 x 128 (the
+ * last block of a row or column may be smaller).  The quantisers below take
+ * the smallest power of two s (at least 2^-126) with max |x| <= 448 s, so
+ * x / s is exact and the only rounding is e4m3's, to nearest even; a block
+ * that holds a NaN or an infinity gets a NaN scale and NaN values.  The
+ * products take any fp32 scales (a checkpoint's, for instance).
+ * Layouts, row-major and contiguous:
+ *   activations  q [rows, cols] e4m3,    scales [ceil(cols/128), rows] f32
+ *   weights      q [E, rows, cols] e4m3, scales [E, ceil(rows/128), ceil(cols/128)] f32
+ * Limits: rows of activations < 2^31; widths multiples of 16 (else
+ * MOE_ERR_UNSUPPORTED); every pointer but offsets 16-byte aligned.
+ */
+
+/* Quantises activations x [rows, cols] (dtype MOE_F32 or MOE_BF16). */
+MOE_API moe_status moe_quantize_rows(int32_t dtype, const void *x, int64_t rows, int32_t cols, void *q,
+                                     float *scales, moe_stream_t stream);
+
+/*
+ * Quantises weights W [E, rows, cols] (dtype MOE_F32 or MOE_BF16).  With
+ * transpose = 1 writes the transposed matrices, q [E, cols, rows] and
+ * scales [E, ceil(cols/128), ceil(rows/128)], whose product with a quantised
+ * output gradient is the input gradient (the same values and scales, so it
+ * is the gradient of the product with the untransposed form).
+ */
+MOE_API moe_status moe_quantize_weights(int32_t dtype, const void *W, int32_t E, int32_t rows, int32_t cols,
+                                        int32_t transpose, void *q, float *scales, moe_stream_t stream);
+
+/*
+ * Ragged grouped product (course module sec. 2.2, "each expert runs once on
+ * its slice"): for the rows r = offsets[e] .. offsets[e+1]-1 of a
+ *   out[r, c] = sum_j a[r, j] w[e, c, j],  a [rows, k], w [E, n, k] quantised
+ * as above, out [rows, n] in out_dtype (MOE_F32 or MOE_BF16).  Products and
+ * sums in fp32, rounded once at the end.  offsets [E+1] is read on the device
+ * and held inside 0 .. rows; rows outside every slice are left as they were.
+ * E <= 256.  dev_status (may be NULL): MOE_ERR_TIMEOUT.  No workspace.
+ */
+MOE_API moe_status moe_expert_matmul_fp8(int64_t rows, int32_t n, int32_t k, int32_t E, const void *a_q,
+                                         const float *a_scales, const int32_t *offsets, const void *w_q,
+                                         const float *w_scales, int32_t out_dtype, void *out,
+                                         int32_t *dev_status, moe_stream_t stream);
+
+/* Quantised expert weights of moe_expert_ffn_fp8, shapes as W1, W3, W2, b1
+ * and b2 above; the biases are bf16 and may be NULL, W3 and its scales are
+ * SwiGLU only, b1 GELU only. */
+typedef struct {
+    const void *W1;
+    const float *W1_scales;
+    const void *W3;
+    const float *W3_scales;
+    const void *W2;
+    const float *W2_scales;
+    const void *b1;
+    const void *b2;
+} moe_fp8_experts;
+
+/* Workspace bytes moe_expert_ffn_fp8 needs for cfg (0 if it does not accept cfg). */
+MOE_API size_t moe_expert_ffn_fp8_workspace_size(const moe_config *cfg);
+
+/*
+ * moe_expert_ffn on quantised weights: x_sorted (bf16) is quantised by rows,
+ * the hidden activations h = act(...) are formed in fp32 and quantised by
+ * rows in the first product's epilogue, y_sorted (bf16) = h W2^T + b2.  cfg
+ * as for moe_expert_ffn, with dtype MOE_BF16 and d_model and d_ff multiples
+ * of 16 (else MOE_ERR_UNSUPPORTED).  Rows of y_sorted outside every slice are
+ * left as they were.  A forward only: a training step keeps bf16 weights and
+ * takes its gradients from moe_backward.
+ */
+MOE_API moe_status moe_expert_ffn_fp8(const moe_config *cfg, const void *x_sorted, const int32_t *offsets,
+                                      const moe_fp8_experts *w, void *y_sorted, int32_t *dev_status, void *ws,
+                                      size_t ws_bytes, moe_stream_t stream);
+
+/* Scores of moe_balance_loss. */
+#define MOE_SCORES_SOFTMAX 0 /* p_n = softmax(z_n) */
+#define MOE_SCORES_SIGMOID 1 /* p_n = sigmoid(z_n) / sum_e sigmoid(z_{n,e}) */
+
+/* Workspace bytes moe_balance_loss needs (0 for sizes it does not accept). */
+MOE_API size_t moe_balance_loss_workspace_size(int64_t N, int32_t E, int32_t S);
+
+/*
+ * Balance loss over sequences, with per-expert counts (course module sec.
+ * 2.3 with the averages taken over one sequence instead of the batch).  The
+ * tokens seq_offsets[s] .. seq_offsets[s+1]-1 form sequence s (seq_offsets
+ * [S+1], device; NULL with S = 1: all N tokens); a token whose token_mask
+ * byte is 0 (padding; mask [N] or NULL) counts for nothing, whatever its
+ * logits and ids hold.  With T_s counted tokens, p_n the scores of the logits
+ * z [N, E] (dtype MOE_F32 or MOE_BF16) and cnt_{s,e} the assignments to e in
+ * topk_ids [N, k]:
+ *   L = 1/S' sum_{s: T_s > 0} E sum_e (cnt_{s,e} / T_s) (sum_n p_{n,e} / T_s)
+ * over the S' sequences with a counted token: k at perfect balance, and
+ * moe_aux_loss's value for one unpadded sequence and softmax scores.  (L / k
+ * is the sequence-wise loss normalised to 1 at balance.)  Logits of -inf
+ * score 0; a token with nothing else scores 0 throughout.  Writes loss_out
+ * [1], counts_out [S, E] (cnt, int32) and seq_weight_out [S] (E / (S' T_s^2),
+ * 0 without counted tokens), which the gradient below takes.  Sums over
+ * tokens are fixed-order fp32 inside a chunk and fp64 above it: equal inputs
+ * give equal bits.  dev_status (may be NULL): an id outside [0, E) of a
+ * counted token is left out and sets MOE_ERR_BAD_EXPERT_ID; seq_offsets that
+ * decrease or leave 0 .. N set MOE_ERR_INVALID_ARG (the outputs are then
+ * meaningless).  E <= 256, k <= min(E, 16), N k < 2^31.
+ */
+MOE_API moe_status moe_balance_loss(int32_t dtype, int32_t scores, const void *logits, const int32_t *topk_ids,
+                                    const int32_t *seq_offsets, const uint8_t *token_mask, int64_t N, int32_t E,
+                                    int32_t k, int32_t S, float *loss_out, int32_t *counts_out,
+                                    float *seq_weight_out, int32_t *dev_status, void *ws, size_t ws_bytes,
+                                    moe_stream_t stream);
+
+/*
+ * Gradient of coef * dloss * L in the logits: dlogits [N, E] fp32,
+ * overwritten; zero for padding and for tokens of no sequence.  The counts
+ * are piecewise constant and carry no gradient (course module sec. 2.4).
+ * counts and seq_weight are moe_balance_loss's for the same logits,
+ * seq_offsets and token_mask; dloss (device scalar, may be NULL: 1) is an
+ * upstream gradient.  No workspace.
+ */
+MOE_API moe_status moe_balance_loss_backward(int32_t dtype, int32_t scores, const void *logits,
+                                             const int32_t *seq_offsets, const uint8_t *token_mask, int64_t N,
+                                             int32_t E, int32_t S, const int32_t *counts, const float *seq_weight,
+                                             float coef, const float *dloss, float *dlogits, moe_stream_t stream);
+
+/*
  * Failure-detection check (the pages have no counterpart): launches one CTA
  * that waits on an mbarrier nothing ever arrives at, through the same
  * bounded wait every tcgen05 kernel of the library uses.  After the wait

@@ -11,15 +11,19 @@ The functions carry the names of the C entry points in ``include/moe.h``:
 ``moe_aux_loss``, ``moe_forward`` and ``moe_workspace_size``, plus the
 shared expert (``moe_shared_ffn``, ``moe_combine_shared``) and the router
 z-loss (``moe_router_z_loss``; ``moe_forward`` with ``shared=`` or
-``z_loss=True`` calls ``moe_forward_ex``).  Symbols follow
+``z_loss=True`` calls ``moe_forward_ex``), the experts on 8-bit weights
+(``moe_quantize_rows``, ``moe_quantize_weights``, ``moe_expert_matmul_fp8``,
+``moe_expert_ffn_fp8``) and the balance loss over sequences with its gradient
+(``moe_balance_loss``, ``moe_balance_loss_backward``).  Symbols follow
 the course module "Mixture of Experts: routing, sorted dispatch, Switch aux
 loss, aux-free bias" (sec. 2): N, E, k, d_model, d_ff, W_g, b_e.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
-from typing import Dict, Optional, Sequence
+from typing import Dict, Optional, Sequence, Tuple
 
 import torch
 
@@ -28,6 +32,7 @@ LIB_PATH = os.path.join(HERE, "libmoe.so")
 
 ROUTERS = {"softmax_topk": 0, "topk_softmax": 1, "sigmoid": 2}
 ACTS = {"gelu": 0, "swiglu": 1}
+SCORES = {"softmax": 0, "sigmoid": 1}
 DTYPES = {"f32": 0, "bf16": 1}
 TORCH_DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_CUDA",
@@ -38,7 +43,9 @@ EXPORTS = ("moe_status_string", "moe_last_error", "moe_version", "moe_workspace_
            "moe_dispatch", "moe_dispatch_noalloc", "moe_expert_ffn", "moe_combine", "moe_aux_loss",
            "moe_forward", "moe_shared_ffn", "moe_combine_shared", "moe_router_z_loss", "moe_forward_ex",
            "moe_backward_workspace_size", "moe_backward", "moe_permute_rows", "moe_selftest_wait_timeout",
-           "moe_forward_partials", "moe_aux_from_partials")
+           "moe_forward_partials", "moe_aux_from_partials", "moe_quantize_rows", "moe_quantize_weights",
+           "moe_expert_matmul_fp8", "moe_expert_ffn_fp8_workspace_size", "moe_expert_ffn_fp8",
+           "moe_balance_loss_workspace_size", "moe_balance_loss", "moe_balance_loss_backward")
 # ceil(N / 32) * E limit of moe_dispatch_noalloc (MOE_NOALLOC_DISPATCH_MAX_SLOTS)
 NOALLOC_DISPATCH_MAX_SLOTS = 1 << 19
 
@@ -65,6 +72,12 @@ class MoeGrads(ctypes.Structure):
     """Mirror of ``moe_grads`` in include/moe.h (fp32 device pointers)."""
     _fields_ = [(name, ctypes.c_void_p) for name in
                 ("dx", "dW_g", "dW1", "db1", "dW3", "dW2", "db2", "dWs1", "dbs1", "dWs3", "dWs2", "dbs2")]
+
+
+class Fp8Experts(ctypes.Structure):
+    """Mirror of ``moe_fp8_experts`` in include/moe.h (device pointers)."""
+    _fields_ = [(name, ctypes.c_void_p) for name in
+                ("W1", "W1_scales", "W3", "W3_scales", "W2", "W2_scales", "b1", "b2")]
 
 
 class MoeError(RuntimeError):
@@ -135,6 +148,24 @@ def library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.moe_backward.restype = st
     lib.moe_permute_rows.argtypes = [ctypes.c_int32, vp, i32p, vp, ctypes.c_int64, ctypes.c_int32, vp]
     lib.moe_permute_rows.restype = st
+    i32, i64, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+    lib.moe_quantize_rows.argtypes = [i32, vp, i64, i32, vp, f32p, vp]
+    lib.moe_quantize_rows.restype = st
+    lib.moe_quantize_weights.argtypes = [i32, vp, i32, i32, i32, i32, vp, f32p, vp]
+    lib.moe_quantize_weights.restype = st
+    lib.moe_expert_matmul_fp8.argtypes = [i64, i32, i32, i32, vp, f32p, i32p, vp, f32p, i32, vp, i32p, vp]
+    lib.moe_expert_matmul_fp8.restype = st
+    lib.moe_expert_ffn_fp8_workspace_size.argtypes = [cfgp]
+    lib.moe_expert_ffn_fp8_workspace_size.restype = sz
+    lib.moe_expert_ffn_fp8.argtypes = [cfgp, vp, i32p, ctypes.POINTER(Fp8Experts), vp, i32p, vp, sz, vp]
+    lib.moe_expert_ffn_fp8.restype = st
+    lib.moe_balance_loss_workspace_size.argtypes = [i64, i32, i32]
+    lib.moe_balance_loss_workspace_size.restype = sz
+    lib.moe_balance_loss.argtypes = [i32, i32, vp, i32p, i32p, vp, i64, i32, i32, i32, f32p, i32p, f32p, i32p, vp, sz,
+                                     vp]
+    lib.moe_balance_loss.restype = st
+    lib.moe_balance_loss_backward.argtypes = [i32, i32, vp, i32p, vp, i64, i32, i32, i32p, f32p, f32, f32p, f32p, vp]
+    lib.moe_balance_loss_backward.restype = st
     lib.moe_selftest_wait_timeout.argtypes = [i32p, vp]
     lib.moe_selftest_wait_timeout.restype = st
     if path is None:
@@ -378,6 +409,227 @@ def moe_backward(cfg: MoeConfig, x: torch.Tensor, W_g: torch.Tensor, W1: torch.T
                                 _stream(stream))
     _check(rc, "moe_backward")
     return out
+
+
+# ------------------------------------------- block-scaled e4m3, balance loss
+
+def _fp8_blocks(n: int) -> int:
+    return -(-n // 128)
+
+
+def _on(t: torch.Tensor, stream):
+    """The device of t, and the given stream, current for a call's allocations and launches."""
+    if not t.is_cuda:
+        raise ValueError("tensor arguments must live on a CUDA device")
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError(f"stream of {stream.device} for tensors on {t.device}")
+        return torch.cuda.stream(stream)
+    if t.device.index != torch.cuda.current_device():
+        return torch.cuda.device(t.device)
+    return contextlib.nullcontext()
+
+
+def _arg(where: str, name: str, t: torch.Tensor, dtype, shape, device) -> ctypes.c_void_p:
+    """Pointer of a tensor argument after checking its type, shape, device and layout."""
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{where}: {name} must be {dtype} of shape {list(shape)}, got {t.dtype} of {list(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{where}: {name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be contiguous")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _float_dtype(where: str, name: str, t: torch.Tensor) -> int:
+    if t.dtype == torch.bfloat16:
+        return 1
+    if t.dtype == torch.float32:
+        return 0
+    raise ValueError(f"{where}: {name} must be float32 or bfloat16, got {t.dtype}")
+
+
+def _aligned_bytes(n: int, device) -> torch.Tensor:
+    """n device bytes on a 256-byte boundary."""
+    raw = torch.empty(n + 256, dtype=torch.uint8, device=device)
+    off = (-raw.data_ptr()) % 256
+    return raw[off:off + n]
+
+
+def moe_quantize_rows(x: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Activations x [rows, cols] (f32 or bf16) as (q [rows, cols] e4m3, scales [ceil(cols/128), rows] f32):
+    one power-of-two scale per row and 128 columns, x ~ q * scale."""
+    where = "moe_quantize_rows"
+    if x.dim() != 2:
+        raise ValueError(f"{where}: x must be [rows, cols]")
+    dtype, dev = _float_dtype(where, "x", x), x.device
+    rows, cols = x.shape
+    with _on(x, stream):
+        q = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=dev)
+        scales = torch.empty((_fp8_blocks(cols), rows), dtype=torch.float32, device=dev)
+        rc = library().moe_quantize_rows(dtype, _ptr(x), rows, cols, _ptr(q), _ptr(scales), _stream())
+    _check(rc, where)
+    return q, scales
+
+
+def moe_quantize_weights(W: torch.Tensor, transpose: bool = False, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Weights W [E, rows, cols] (f32 or bf16) as (q e4m3, scales f32) with one power-of-two scale per 128 x 128
+    block; transpose=True gives the transposed matrices [E, cols, rows], the operand of the input gradient."""
+    where = "moe_quantize_weights"
+    if W.dim() != 3:
+        raise ValueError(f"{where}: W must be [E, rows, cols]")
+    dtype, dev = _float_dtype(where, "W", W), W.device
+    E, rows, cols = W.shape
+    r, c = (cols, rows) if transpose else (rows, cols)
+    with _on(W, stream):
+        q = torch.empty((E, r, c), dtype=torch.float8_e4m3fn, device=dev)
+        scales = torch.empty((E, _fp8_blocks(r), _fp8_blocks(c)), dtype=torch.float32, device=dev)
+        rc = library().moe_quantize_weights(dtype, _ptr(W), E, rows, cols, int(bool(transpose)), _ptr(q),
+                                            _ptr(scales), _stream())
+    _check(rc, where)
+    return q, scales
+
+
+def moe_expert_matmul_fp8(a: Tuple[torch.Tensor, torch.Tensor], offsets: torch.Tensor,
+                          w: Tuple[torch.Tensor, torch.Tensor], out_dtype: torch.dtype = torch.bfloat16,
+                          out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                          stream=None) -> torch.Tensor:
+    """Rows offsets[e] .. offsets[e+1]-1 of a times w[e]^T -> [rows, n] (bf16 or f32).
+
+    a = (q [rows, k], scales) from moe_quantize_rows, w = (q [E, n, k], scales) from moe_quantize_weights
+    (or any fp32 scales).  Rows outside every slice keep what ``out`` held."""
+    where = "moe_expert_matmul_fp8"
+    (aq, asc), (wq, wsc) = a, w
+    if aq.dim() != 2 or wq.dim() != 3:
+        raise ValueError(f"{where}: a must be [rows, k] and w [E, n, k]")
+    (rows, k), (E, n, _), dev, e4m3, f32 = aq.shape, wq.shape, aq.device, torch.float8_e4m3fn, torch.float32
+    kb = _fp8_blocks(k)
+    if out_dtype not in (torch.bfloat16, f32):
+        raise ValueError(f"{where}: out_dtype must be bfloat16 or float32, got {out_dtype}")
+    with _on(aq, stream):
+        out = out if out is not None else torch.empty((rows, n), dtype=out_dtype, device=dev)
+        rc = library().moe_expert_matmul_fp8(
+            rows, n, k, E, _arg(where, "a", aq, e4m3, (rows, k), dev),
+            _arg(where, "a's scales", asc, f32, (kb, rows), dev),
+            _arg(where, "offsets", offsets, torch.int32, (E + 1,), dev), _arg(where, "w", wq, e4m3, (E, n, k), dev),
+            _arg(where, "w's scales", wsc, f32, (E, _fp8_blocks(n), kb), dev), int(out_dtype == torch.bfloat16),
+            _arg(where, "out", out, out_dtype, (rows, n), dev),
+            _arg(where, "status", status, torch.int32, (1,), dev) if status is not None else None, _stream())
+    _check(rc, where)
+    return out
+
+
+def moe_expert_ffn_fp8_workspace(cfg: MoeConfig, device=None) -> torch.Tensor:
+    """A device workspace for moe_expert_ffn_fp8 (256-byte aligned)."""
+    n = int(library().moe_expert_ffn_fp8_workspace_size(ctypes.byref(cfg)))
+    if n == 0:
+        raise MoeError(2, "moe_expert_ffn_fp8_workspace_size")
+    return _aligned_bytes(n, device or "cuda")
+
+
+def moe_expert_ffn_fp8(cfg: MoeConfig, x_sorted: torch.Tensor, offsets: torch.Tensor,
+                       W1: Tuple[torch.Tensor, torch.Tensor], W2: Tuple[torch.Tensor, torch.Tensor],
+                       b1: Optional[torch.Tensor] = None, W3: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+                       b2: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                       status: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                       stream=None) -> torch.Tensor:
+    """moe_expert_ffn on quantised weights: W1, W2 (and W3) are (q, scales) pairs of moe_quantize_weights, x_sorted
+    and the result bf16.  Rows outside every slice keep what ``out`` held."""
+    where, dev = "moe_expert_ffn_fp8", x_sorted.device
+    e4m3, f32, bf16 = torch.float8_e4m3fn, torch.float32, torch.bfloat16
+    E, d, F, A = cfg.E, cfg.d_model, cfg.d_ff, cfg.N * cfg.k
+
+    def pair(name, w, rows, cols):
+        if w is None:
+            return None, None
+        return (_arg(where, name, w[0], e4m3, (E, rows, cols), dev).value,
+                _arg(where, name + "'s scales", w[1], f32, (E, _fp8_blocks(rows), _fp8_blocks(cols)), dev).value)
+
+    def one(name, t, dtype, shape):
+        return None if t is None else _arg(where, name, t, dtype, shape, dev).value
+
+    with _on(x_sorted, stream):
+        ws = ws if ws is not None else moe_expert_ffn_fp8_workspace(cfg, dev)
+        out = out if out is not None else torch.empty((A, d), dtype=bf16, device=dev)
+        w = Fp8Experts(*pair("W1", W1, F, d), *pair("W3", W3, F, d), *pair("W2", W2, d, F),
+                       one("b1", b1, bf16, (E, F)), one("b2", b2, bf16, (E, d)))
+        rc = library().moe_expert_ffn_fp8(
+            ctypes.byref(cfg), _arg(where, "x_sorted", x_sorted, bf16, (A, d), dev),
+            _arg(where, "offsets", offsets, torch.int32, (E + 1,), dev), ctypes.byref(w),
+            _arg(where, "out", out, bf16, (A, d), dev), one("status", status, torch.int32, (1,)), _ptr(ws),
+            ws.numel(), _stream())
+    _check(rc, where)
+    return out
+
+
+def _sequences(where: str, logits: torch.Tensor, seq_offsets, token_mask):
+    """(N, E, S, seq_offsets pointer, mask pointer) of the balance loss."""
+    if logits.dim() != 2:
+        raise ValueError(f"{where}: logits must be [N, E]")
+    N, E = logits.shape
+    if seq_offsets is not None and (seq_offsets.dim() != 1 or seq_offsets.numel() < 2):
+        raise ValueError(f"{where}: seq_offsets must be [S + 1] with S >= 1")
+    S = seq_offsets.numel() - 1 if seq_offsets is not None else 1
+    off = (_arg(where, "seq_offsets", seq_offsets, torch.int32, (S + 1,), logits.device)
+           if seq_offsets is not None else None)
+    mask = None
+    if token_mask is not None:
+        mask = _arg(where, "token_mask", token_mask, torch.uint8 if token_mask.dtype == torch.uint8 else torch.bool,
+                    (N,), logits.device)
+    return N, E, S, off, mask
+
+
+def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, seq_offsets: Optional[torch.Tensor] = None,
+                     token_mask: Optional[torch.Tensor] = None, scores: str = "softmax",
+                     ws: Optional[torch.Tensor] = None, stream=None) -> Dict[str, torch.Tensor]:
+    """Balance loss over sequences from router logits [N, E] (f32 or bf16) and topk_ids [N, k] int32.
+
+    seq_offsets [S + 1] int32 (default: one sequence), token_mask [N] bool or uint8 (False: padding), scores
+    "softmax" or "sigmoid" (normalised).  Returns loss [1], counts [S, E] int32, seq_weight [S] (for the gradient)
+    and status [1] int32 (6: an expert id out of range, 1: bad seq_offsets)."""
+    where, dev = "moe_balance_loss", logits.device
+    dtype = _float_dtype(where, "logits", logits)
+    N, E, S, off, mask = _sequences(where, logits, seq_offsets, token_mask)
+    if topk_ids.dim() != 2:
+        raise ValueError(f"{where}: topk_ids must be [N, k]")
+    k = topk_ids.shape[1]
+    with _on(logits, stream):
+        if ws is None:
+            n = int(library().moe_balance_loss_workspace_size(N, E, S))
+            if n == 0:
+                raise MoeError(2, "moe_balance_loss_workspace_size")
+            ws = _aligned_bytes(n, dev)
+        loss = torch.empty(1, dtype=torch.float32, device=dev)
+        counts = torch.empty((S, E), dtype=torch.int32, device=dev)
+        weight = torch.empty(S, dtype=torch.float32, device=dev)
+        status = torch.zeros(1, dtype=torch.int32, device=dev)
+        rc = library().moe_balance_loss(dtype, SCORES[scores], _ptr(logits),
+                                        _arg(where, "topk_ids", topk_ids, torch.int32, (N, k), dev), off, mask, N, E,
+                                        k, S, _ptr(loss), _ptr(counts), _ptr(weight), _ptr(status), _ptr(ws),
+                                        ws.numel(), _stream())
+    _check(rc, where)
+    return {"loss": loss, "counts": counts, "seq_weight": weight, "status": status}
+
+
+def moe_balance_loss_backward(logits: torch.Tensor, fwd: Dict[str, torch.Tensor],
+                              seq_offsets: Optional[torch.Tensor] = None, token_mask: Optional[torch.Tensor] = None,
+                              scores: str = "softmax", coef: float = 1.0, dloss: Optional[torch.Tensor] = None,
+                              stream=None) -> torch.Tensor:
+    """dlogits [N, E] f32 of coef * dloss * loss, for the same arguments as moe_balance_loss and its result ``fwd``
+    (dloss: an upstream gradient [1] f32 on the device)."""
+    where, dev = "moe_balance_loss_backward", logits.device
+    dtype = _float_dtype(where, "logits", logits)
+    N, E, S, off, mask = _sequences(where, logits, seq_offsets, token_mask)
+    with _on(logits, stream):
+        dlogits = torch.empty((N, E), dtype=torch.float32, device=dev)
+        rc = library().moe_balance_loss_backward(
+            dtype, SCORES[scores], _ptr(logits), off, mask, N, E, S,
+            _arg(where, "counts", fwd["counts"], torch.int32, (S, E), dev),
+            _arg(where, "seq_weight", fwd["seq_weight"], torch.float32, (S,), dev), float(coef),
+            _arg(where, "dloss", dloss, torch.float32, (1,), dev) if dloss is not None else None, _ptr(dlogits),
+            _stream())
+    _check(rc, where)
+    return dlogits
 
 
 def moe_selftest_wait_timeout(stream=None) -> int:

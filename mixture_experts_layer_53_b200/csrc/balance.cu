@@ -1,0 +1,495 @@
+// balance.cu -- balance loss over sequences, per-expert counts, and the
+// gradient of the router's logits.
+//
+// With T_s valid tokens in sequence s, scores p_n = softmax(z_n) or
+// sigmoid(z_n) / sum_j sigmoid(z_{n,j}), cnt_{s,e} the assignments to e and
+// P_{s,e} = sum_n p_{n,e} over the sequence's valid tokens:
+//   L = 1/S' sum_{s: T_s > 0} E / T_s^2 sum_e cnt_{s,e} P_{s,e}
+//   dL/dz_{n,e} = p_{n,e} m_{n,e} (c_{s,e} - sum_j p_{n,j} c_{s,j}),
+//   c_{s,e} = cnt_{s,e} E / (S' T_s^2), m = 1 (softmax), 1 - sigmoid(z_{n,e}),
+// S' the sequences with a valid token (course module "Mixture of Experts",
+// sec. 2.3, with the averages over one sequence instead of the batch).
+//
+// A token's E scores lie on G lanes, 4 * NV consecutive-by-four experts per
+// lane, so that a lane keeps its experts for all tokens it visits and P_{s,e}
+// is summed in its registers.  Both passes are bound by reading the logits
+// (and writing the gradient); the exponentials run on the special-function
+// unit.  Everything is summed in a fixed order (floats) or in integers: equal
+// inputs give equal bits.
+#include <cuda_runtime.h>
+
+#include <type_traits>
+
+#include "common.cuh"
+#include "host_util.h"
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kUnroll = 4;       // tokens a lane group loads at once
+constexpr int kMinChunk = 32;
+constexpr int kMaxChunks = 1184;  // 148 SMs x 8 CTAs
+
+__host__ __device__ __forceinline__ int64_t align256(int64_t b) { return (b + 255) & ~static_cast<int64_t>(255); }
+
+// Tokens [chunk c * C, (c + 1) * C) may touch several sequences.  The pairs
+// (c, s) with common tokens increase in both, so c + s numbers them.
+struct Plan {
+    int64_t chunk, chunks, slots, ticket, psum, cnt, tok, tokens, dot, total;
+    int groups;  // 32-expert groups of the second kernel
+};
+
+Plan make_plan(int64_t N, int E, int S)
+{
+    Plan p{};
+    const int64_t even = (N + kMaxChunks - 1) / kMaxChunks;
+    p.chunk = max64(kMinChunk, (even + 7) / 8 * 8);
+    p.chunks = max64(1, (N + p.chunk - 1) / p.chunk);
+    p.slots = p.chunks + S;
+    p.groups = (E + 31) / 32;
+    int64_t o = 0;
+    auto take = [&o](int64_t bytes) {
+        const int64_t at = o;
+        o += align256(bytes);
+        return at;
+    };
+    p.ticket = take(4);
+    p.psum = take(p.slots * E * 4);
+    p.cnt = take(p.slots * E * 4);
+    p.tok = take(p.slots * 4);
+    p.tokens = take(static_cast<int64_t>(S) * 4);
+    p.dot = take(static_cast<int64_t>(S) * p.groups * 8);
+    p.total = o;
+    return p;
+}
+
+struct Seqs {
+    const int32_t *off;
+    int64_t N;
+    // boundary i of the sequences, held inside 0 .. N
+    __device__ __forceinline__ int64_t at(int i) const
+    {
+        if (!off) return i == 0 ? 0 : N;
+        return min64(max64(__ldg(off + i), 0), N);
+    }
+    // the last sequence that starts at or before token n (0 if none does)
+    __device__ __forceinline__ int find(int64_t n, int S) const
+    {
+        int lo = 0, hi = S - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (at(mid) <= n) lo = mid;
+            else hi = mid - 1;
+        }
+        return lo;
+    }
+};
+
+// Four consecutive logits from expert e on; -inf past E.
+__device__ __forceinline__ float4 load4(const float *p, int e, int E, bool vec)
+{
+    const float ninf = -INFINITY;
+    if (vec) return e < E ? __ldcs(reinterpret_cast<const float4 *>(p + e)) : make_float4(ninf, ninf, ninf, ninf);
+    return make_float4(e < E ? p[e] : ninf, e + 1 < E ? p[e + 1] : ninf, e + 2 < E ? p[e + 2] : ninf,
+                       e + 3 < E ? p[e + 3] : ninf);
+}
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p, int e, int E, bool vec)
+{
+    const float ninf = -INFINITY;
+    if (vec) {
+        if (e >= E) return make_float4(ninf, ninf, ninf, ninf);
+        const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p + e));
+        return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                           __uint_as_float(v.y & 0xFFFF0000u));
+    }
+    return make_float4(e < E ? to_f32(p[e]) : ninf, e + 1 < E ? to_f32(p[e + 1]) : ninf,
+                       e + 2 < E ? to_f32(p[e + 2]) : ninf, e + 3 < E ? to_f32(p[e + 3]) : ninf);
+}
+
+template <int G> __device__ __forceinline__ float group_sum(float v)
+{
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+template <int G> __device__ __forceinline__ float group_max(float v)
+{
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+constexpr float kLog2e = 1.44269504f;
+
+// Normalised scores of one token, in place of its logits z; with `slope` also
+// m = 1 - sigmoid(z).  Every lane of the warp takes part.  A token whose
+// logits are all -inf has no scores: p = 0.  The exponent is the rounded
+// product of z - max (or |z|) and log2 e, so its error is relative to it:
+// about 1e-7 for the scores that matter, 6e-8 |z - max| for small ones.
+template <int G, int NV, bool SIGMOID>
+__device__ __forceinline__ void scores(float (&z)[4 * NV], float *m)
+{
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4 * NV; ++i) top = fmaxf(top, z[i]);
+    top = group_max<G>(top);
+    float sum = 0.0f;
+    if constexpr (!SIGMOID) {
+        const float shift = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+        for (int i = 0; i < 4 * NV; ++i) {
+            z[i] = ex2_approx((z[i] - shift) * kLog2e);
+            sum += z[i];
+        }
+    } else {
+        // sigma(z) = a / (1 + a') with exponentials of non-positive arguments
+        // only.  If every logit is far below zero the sigmoids underflow but
+        // their ratios do not: e^-top then multiplies all of them.
+        const float low = (top < -20.0f && top != -INFINITY) ? top : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4 * NV; ++i) {
+            const float e = ex2_approx(fabsf(z[i]) * -kLog2e);
+            const float r = rcp_approx(1.0f + e);
+            const bool pos = z[i] >= 0.0f;
+            if (m) m[i] = (pos ? e : 1.0f) * r;
+            z[i] = low != 0.0f ? ex2_approx((z[i] - low) * kLog2e) * r : (pos ? 1.0f : e) * r;
+            sum += z[i];
+        }
+    }
+    sum = group_sum<G>(sum);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int i = 0; i < 4 * NV; ++i) z[i] *= inv;
+}
+
+template <typename T, int G, int NV, bool SIGMOID>
+__global__ void __launch_bounds__(kThreads) balance_partial_kernel(const BalanceArgs a, const Plan p)
+{
+    pdl_enter();
+    __shared__ float red[kWarps][G * 4 * NV];
+    __shared__ int cnt[kMaxE];
+    __shared__ int valid;
+    constexpr int GROUPS = kThreads / G;
+    uint8_t *ws = static_cast<uint8_t *>(a.ws);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int group = threadIdx.x / G, q = threadIdx.x % G;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *reinterpret_cast<uint32_t *>(ws + p.ticket) = 0;
+    const Seqs seqs{a.seq_offsets, a.N};
+    const T *logits = static_cast<const T *>(a.logits);
+    const bool vec = a.E % 4 == 0;
+    const int64_t c = blockIdx.x, begin = c * p.chunk, end = min64(begin + p.chunk, a.N);
+    for (int s = seqs.find(begin, a.S); s < a.S; ++s) {
+        const int64_t lo = max64(seqs.at(s), begin), hi = min64(seqs.at(s + 1), end);
+        if (lo >= end) break;
+        if (lo >= hi) continue;
+        __syncthreads();  // the last segment's shared sums have been read
+        for (int i = threadIdx.x; i < a.E; i += kThreads) cnt[i] = 0;
+        if (threadIdx.x == 0) valid = 0;
+        __syncthreads();
+        float sum[4 * NV];
+#pragma unroll
+        for (int i = 0; i < 4 * NV; ++i) sum[i] = 0.0f;
+        int mine = 0;
+        for (int64_t n0 = lo; n0 < hi; n0 += GROUPS * kUnroll) {
+            float4 v[kUnroll][NV];
+            bool use[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int64_t n = n0 + u * GROUPS + group;
+                use[u] = n < hi && (!a.mask || a.mask[n] != 0);
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+                    v[u][j] = use[u] ? load4(logits + n * a.E, (j * G + q) * 4, a.E, vec)
+                                     : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                float z[4 * NV];
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    z[4 * j] = v[u][j].x;
+                    z[4 * j + 1] = v[u][j].y;
+                    z[4 * j + 2] = v[u][j].z;
+                    z[4 * j + 3] = v[u][j].w;
+                }
+                scores<G, NV, SIGMOID>(z, nullptr);  // an unused token: all -inf, p = 0
+                mine += use[u] && q == 0;
+#pragma unroll
+                for (int i = 0; i < 4 * NV; ++i) sum[i] += z[i];
+            }
+        }
+        const int64_t ids = (hi - lo) * a.k;
+        for (int64_t i = threadIdx.x; i < ids; i += kThreads) {
+            if (a.mask && a.mask[lo + i / a.k] == 0) continue;
+            const int e = a.ids[lo * a.k + i];
+            if (static_cast<unsigned>(e) < static_cast<unsigned>(a.E)) atomicAdd(&cnt[e], 1);
+            else set_status(a.status, kDevBadExpertId);
+        }
+        if (mine) atomicAdd(&valid, mine);
+        // over the warp's lane groups, then over the warps
+#pragma unroll
+        for (int i = 0; i < 4 * NV; ++i) {
+#pragma unroll
+            for (int o = G; o < 32; o <<= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+        }
+        if (lane < G) {
+#pragma unroll
+            for (int i = 0; i < 4 * NV; ++i) red[warp][(i / 4 * G + q) * 4 + i % 4] = sum[i];
+        }
+        __syncthreads();
+        const int64_t slot = c + s;
+        for (int e = threadIdx.x; e < a.E; e += kThreads) {
+            float t = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) t += red[w][e];
+            reinterpret_cast<float *>(ws + p.psum)[slot * a.E + e] = t;
+            reinterpret_cast<int *>(ws + p.cnt)[slot * a.E + e] = cnt[e];
+        }
+        if (threadIdx.x == 0) reinterpret_cast<int *>(ws + p.tok)[slot] = valid;
+    }
+}
+
+// One CTA per (sequence, 32 experts): its slots summed in fp64 (scores) and
+// integers, counts written, its share of sum_e cnt P kept; the last CTA to
+// finish forms the loss and the sequences' weights.
+__global__ void __launch_bounds__(1024) balance_finish_kernel(const BalanceArgs a, const Plan p)
+{
+    pdl_enter();
+    __shared__ double dsum[32][33];
+    __shared__ int isum[32][33];
+    __shared__ bool last;
+    uint8_t *ws = static_cast<uint8_t *>(a.ws);
+    const float *psum = reinterpret_cast<const float *>(ws + p.psum);
+    const int *cnt = reinterpret_cast<const int *>(ws + p.cnt), *tok = reinterpret_cast<const int *>(ws + p.tok);
+    int *tokens = reinterpret_cast<int *>(ws + p.tokens);
+    double *dot = reinterpret_cast<double *>(ws + p.dot);
+    uint32_t *ticket = reinterpret_cast<uint32_t *>(ws + p.ticket);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const Seqs seqs{a.seq_offsets, a.N};
+    const int s = static_cast<int>(blockIdx.x / p.groups), gr = static_cast<int>(blockIdx.x % p.groups);
+    const int e = gr * 32 + lane;
+    const int64_t lo = seqs.at(s), hi = seqs.at(s + 1);
+    const int64_t c0 = lo / p.chunk, c1 = hi > lo ? (hi - 1) / p.chunk + 1 : c0;
+    double P = 0.0;
+    int n = 0, T = 0;
+    if (e < a.E) {
+#pragma unroll 4
+        for (int64_t c = c0 + warp; c < c1; c += warps) {
+            P += psum[(c + s) * a.E + e];
+            n += cnt[(c + s) * a.E + e];
+        }
+    }
+    if (gr == 0)
+        for (int64_t c = c0 + threadIdx.x; c < c1; c += blockDim.x) T += tok[c + s];
+    dsum[warp][lane] = P;
+    isum[warp][lane] = n;
+    __syncthreads();
+    if (warp == 0) {
+        for (int w = 1; w < warps; ++w) {
+            P += dsum[w][lane];
+            n += isum[w][lane];
+        }
+        if (e < a.E) a.counts[static_cast<int64_t>(s) * a.E + e] = n;
+        double d = e < a.E ? P * n : 0.0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+        if (lane == 0) dot[static_cast<int64_t>(s) * p.groups + gr] = d;
+    }
+    __syncthreads();
+    T = __reduce_add_sync(0xffffffffu, T);
+    if (lane == 0) isum[warp][0] = T;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        if (gr == 0) {
+            int all = 0;
+            for (int w = 0; w < warps; ++w) all += isum[w][0];
+            tokens[s] = all;
+            // offsets that decrease or leave 0 .. N
+            if (a.seq_offsets && (a.seq_offsets[s] < 0 || a.seq_offsets[s + 1] < a.seq_offsets[s] || a.seq_offsets[s + 1] > a.N))
+                set_status(a.status, 1);
+        }
+        __threadfence();
+        last = atomicAdd(ticket, 1u) + 1u == gridDim.x;
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    // sequences with tokens
+    int full = 0;
+    for (int i = threadIdx.x; i < a.S; i += blockDim.x) full += __ldcg(tokens + i) > 0;
+    full = __reduce_add_sync(0xffffffffu, full);
+    if (lane == 0) isum[warp][0] = full;
+    __syncthreads();
+    full = 0;
+    for (int w = 0; w < warps; ++w) full += isum[w][0];
+    double L = 0.0;
+    for (int i = threadIdx.x; i < a.S; i += blockDim.x) {
+        const double t = __ldcg(tokens + i);
+        double d = 0.0;
+        for (int j = 0; j < p.groups; ++j) d += __ldcg(dot + static_cast<int64_t>(i) * p.groups + j);
+        const double w = t > 0.0 ? a.E / (t * t * full) : 0.0;
+        a.seq_weight[i] = static_cast<float>(w);
+        if (t > 0.0) L += w * d;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    __syncthreads();
+    if (lane == 0) dsum[warp][0] = L;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        L = 0.0;
+        for (int w = 0; w < warps; ++w) L += dsum[w][0];
+        *a.loss = static_cast<float>(L);
+    }
+}
+
+template <typename T, int G, int NV, bool SIGMOID>
+__global__ void __launch_bounds__(kThreads) balance_backward_kernel(const BalanceArgs a, int64_t per_cta)
+{
+    pdl_enter();
+    constexpr int GROUPS = kThreads / G;
+    const int group = threadIdx.x / G, q = threadIdx.x % G;
+    const Seqs seqs{a.seq_offsets, a.N};
+    const T *logits = static_cast<const T *>(a.logits);
+    const bool vec = a.E % 4 == 0;
+    const int64_t begin = blockIdx.x * per_cta, end = min64(begin + per_cta, a.N);
+    const float scale = a.dloss ? a.coef * *a.dloss : a.coef;
+    int s = seqs.find(min64(begin, a.N - 1), a.S), loaded = -1;
+    int64_t lo = seqs.at(s), hi = seqs.at(s + 1);
+    float c[4 * NV];
+#pragma unroll
+    for (int i = 0; i < 4 * NV; ++i) c[i] = 0.0f;
+    for (int64_t n0 = begin; n0 < end; n0 += GROUPS * kUnroll) {
+        float4 v[kUnroll][NV];
+        bool use[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int64_t n = n0 + u * GROUPS + group;
+            use[u] = n < end && (!a.mask || a.mask[n] != 0);
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                v[u][j] = use[u] ? load4(logits + n * a.E, (j * G + q) * 4, a.E, vec)
+                                 : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int64_t n = n0 + u * GROUPS + group;
+            if (n < end) {
+                while (n >= hi && s + 1 < a.S) {
+                    ++s;
+                    lo = hi;
+                    hi = seqs.at(s + 1);
+                }
+            }
+            const bool in = n >= lo && n < hi;
+            if (in && n < end && loaded != s) {
+                loaded = s;
+                const float w = scale * a.seq_weight[s];
+                const int32_t *cs = a.counts + static_cast<int64_t>(s) * a.E;
+#pragma unroll
+                for (int i = 0; i < 4 * NV; ++i) {
+                    const int e = (i / 4 * G + q) * 4 + i % 4;
+                    c[i] = e < a.E ? w * static_cast<float>(__ldg(cs + e)) : 0.0f;
+                }
+            }
+            float z[4 * NV], m[4 * NV];
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                z[4 * j] = v[u][j].x;
+                z[4 * j + 1] = v[u][j].y;
+                z[4 * j + 2] = v[u][j].z;
+                z[4 * j + 3] = v[u][j].w;
+            }
+            scores<G, NV, SIGMOID>(z, SIGMOID ? m : nullptr);
+            float dot = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4 * NV; ++i) dot = fmaf(z[i], c[i], dot);
+            dot = group_sum<G>(dot);
+            if (n >= end) continue;
+            const bool real = use[u] && in;
+            float *out = a.dlogits + n * a.E;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int e = (j * G + q) * 4;
+                float o[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float g = z[4 * j + i] * (c[4 * j + i] - dot);
+                    if (SIGMOID) g *= m[4 * j + i];
+                    o[i] = real ? g : 0.0f;
+                }
+                if (vec) {
+                    if (e < a.E) __stcs(reinterpret_cast<float4 *>(out + e), make_float4(o[0], o[1], o[2], o[3]));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (e + i < a.E) out[e + i] = o[i];
+                }
+            }
+        }
+    }
+}
+
+// Calls f with the lanes per token and the vectors per lane for E experts.
+template <typename T, bool SIGMOID, typename F> cudaError_t by_width(int E, F &&f)
+{
+    if (E <= 4) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
+    if (E <= 8) return f(std::integral_constant<int, 2>{}, std::integral_constant<int, 1>{});
+    if (E <= 16) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
+    if (E <= 32) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
+    if (E <= 64) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
+    if (E <= 128) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 1>{});
+    return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 2>{});
+}
+
+template <typename T, bool SIGMOID> cudaError_t forward(const BalanceArgs &a, const Plan &p, cudaStream_t s)
+{
+    return by_width<T, SIGMOID>(a.E, [&](auto g, auto nv) {
+        return launch_k(balance_partial_kernel<T, decltype(g)::value, decltype(nv)::value, SIGMOID>,
+                        dim3(static_cast<unsigned>(p.chunks)), dim3(kThreads), 0, s, a, p);
+    });
+}
+
+template <typename T, bool SIGMOID>
+cudaError_t backward(const BalanceArgs &a, int64_t ctas, int64_t per_cta, cudaStream_t s)
+{
+    return by_width<T, SIGMOID>(a.E, [&](auto g, auto nv) {
+        return launch_k(balance_backward_kernel<T, decltype(g)::value, decltype(nv)::value, SIGMOID>,
+                        dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, s, a, per_cta);
+    });
+}
+
+}  // namespace
+
+size_t balance_workspace(int64_t N, int E, int S) { return static_cast<size_t>(make_plan(N, E, S).total); }
+
+cudaError_t launch_balance_loss(const BalanceArgs &a, cudaStream_t s)
+{
+    const Plan p = make_plan(a.N, a.E, a.S);
+    cudaError_t err;
+    if (a.dtype == kF32) err = a.sigmoid ? forward<float, true>(a, p, s) : forward<float, false>(a, p, s);
+    else err = a.sigmoid ? forward<__nv_bfloat16, true>(a, p, s) : forward<__nv_bfloat16, false>(a, p, s);
+    if (err != cudaSuccess) return err;
+    // many chunks to a sequence: a warp each; few: no more warps than chunks
+    const int64_t each = p.chunks / a.S + 1;
+    const int warps = static_cast<int>(min64(32, max64(2, each)));
+    const int64_t ctas = static_cast<int64_t>(a.S) * p.groups;
+    if (ctas >= (static_cast<int64_t>(1) << 31)) return cudaErrorInvalidValue;
+    return launch_k(balance_finish_kernel, dim3(static_cast<unsigned>(ctas)), dim3(32 * warps), 0, s, a, p);
+}
+
+cudaError_t launch_balance_backward(const BalanceArgs &a, int num_sms, cudaStream_t s)
+{
+    if (a.N == 0) return cudaSuccess;
+    const int64_t most = static_cast<int64_t>(num_sms) * 8;
+    const int64_t per_cta = max64(kMinChunk, (a.N + most - 1) / most), ctas = (a.N + per_cta - 1) / per_cta;
+    if (a.dtype == kF32)
+        return a.sigmoid ? backward<float, true>(a, ctas, per_cta, s) : backward<float, false>(a, ctas, per_cta, s);
+    return a.sigmoid ? backward<__nv_bfloat16, true>(a, ctas, per_cta, s)
+                     : backward<__nv_bfloat16, false>(a, ctas, per_cta, s);
+}
+
+}  // namespace moe

@@ -283,6 +283,7 @@ bool make_tmap_bf16_mn(CUtensorMap *m, const void *base, uint64_t inner, uint64_
 bool make_tmap_bf16_mn_rows(CUtensorMap *m, const void *base, uint64_t inner, uint64_t rows, uint64_t ld);
 bool make_tmap_f32_store(CUtensorMap *m, void *base, uint64_t inner, uint64_t rows, uint64_t groups);
 bool make_tmap_bf16_store(CUtensorMap *m, void *base, uint64_t inner, uint64_t rows);
+bool make_tmap_u8(CUtensorMap *m, const void *base, uint64_t inner, uint64_t rows, uint64_t groups, uint32_t box_rows);
 
 // C (fp32) from bf16 operands on tcgen05 (the backward's products on the
 // tensor cores), 128 x 256 tiles:
@@ -330,5 +331,59 @@ cudaError_t launch_ffn_bf16_sm100(const FfnArgs &a, int num_sms, cudaEvent_t mid
 // single CTAs, 128-row m-tiles:
 cudaError_t launch_ffn_bf16_sm100_single(const FfnArgs &a, int num_sms, cudaEvent_t mid, cudaStream_t s);
 cudaError_t launch_ffn_f32_simt(const FfnArgs &a, int num_sms, cudaEvent_t mid, cudaStream_t s);
+
+// ---- block-scaled e4m3 (quantize.cu, gemm_fp8_sm100.cu)
+// x [rows, cols] -> q [rows, cols] e4m3, scales [ceil(cols / 128), rows].
+cudaError_t launch_quantize_rows(int dtype, const void *x, int64_t rows, int cols, void *q, float *scales,
+                                 cudaStream_t s);
+// W [E, rows, cols] -> q [E, rows, cols] e4m3, scales [E, ceil(rows / 128),
+// ceil(cols / 128)]; transpose: both with the last two axes exchanged.
+cudaError_t launch_quantize_weights(int dtype, const void *W, int E, int rows, int cols, int transpose, void *q,
+                                    float *scales, cudaStream_t s);
+
+// Rows offsets[e] .. offsets[e+1]-1 of a [rows, k] times w[e]^T ([E, n, k]):
+// bf16 or fp32 rows, or with SwiGLU (w3) / GELU the quantised hidden
+// activations (out: e4m3 [rows, n], h_scales [ceil(n / 128), rows]).
+enum { kFp8Swiglu = 0, kFp8Gelu = 1, kFp8Bf16 = 2, kFp8F32 = 3 };
+struct Fp8GemmArgs {
+    int epi;
+    const void *a;
+    const float *a_scales;  // [ceil(k / 128), rows]
+    const int32_t *offsets;
+    const void *w;
+    const float *w_scales;  // [E, ceil(n / 128), ceil(k / 128)]
+    const void *w3;         // kFp8Swiglu
+    const float *w3_scales;
+    const void *bias;       // [E, n] bf16 or null
+    void *out;
+    float *h_scales;
+    int32_t *status;
+    int64_t rows;
+    int E, n, k;
+};
+cudaError_t launch_gemm_fp8(const Fp8GemmArgs &a, int num_sms, cudaStream_t s);
+
+// ---- balance loss over sequences (balance.cu)
+struct BalanceArgs {
+    int dtype;                   // of the logits
+    int sigmoid;                 // scores: softmax(z), or sigmoid(z) normalised
+    const void *logits;          // [N, E]
+    const int32_t *ids;          // [N, k] (forward)
+    const int32_t *seq_offsets;  // [S + 1] or null: one sequence of all N tokens
+    const uint8_t *mask;         // [N] or null: 0 = padding
+    int64_t N;
+    int E, k, S;
+    int32_t *counts;             // [S, E]
+    float *seq_weight;           // [S]: E / (S' T_s^2)
+    float *loss;                 // forward
+    int32_t *status;
+    void *ws;
+    const float *dloss;          // backward: device scalar or null (1)
+    float coef;
+    float *dlogits;              // [N, E]
+};
+size_t balance_workspace(int64_t N, int E, int S);
+cudaError_t launch_balance_loss(const BalanceArgs &a, cudaStream_t s);
+cudaError_t launch_balance_backward(const BalanceArgs &a, int num_sms, cudaStream_t s);
 
 }  // namespace moe

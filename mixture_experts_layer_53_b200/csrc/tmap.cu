@@ -97,6 +97,22 @@ bool make_tmap_bf16_store(CUtensorMap *m, void *base, uint64_t inner, uint64_t r
            CUDA_SUCCESS;
 }
 
+// Bytes [groups][rows][inner] (inner contiguous, a multiple of 16) read by
+// boxes of {128 inner, box_rows, 1 group}, 128-byte swizzle, zero fill past
+// the inner extent and past each group's rows: e4m3 operands.
+bool make_tmap_u8(CUtensorMap *m, const void *base, uint64_t inner, uint64_t rows, uint64_t groups, uint32_t box_rows)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {inner, rows, groups};
+    const cuuint64_t strides[2] = {inner, inner * rows};
+    const cuuint32_t box[3] = {128, box_rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // fp32 tensor [groups][rows][inner] (inner contiguous) written by 32 x 32
 // boxes from 128-byte-swizzled shared memory; stores are clipped at the
 // extents.

@@ -1,0 +1,380 @@
+"""Block-scaled e4m3 quantisation, grouped product and expert FFN on the GPU
+against 64-bit references (fp8_reference.py)."""
+import numpy as np
+import pytest
+import torch
+
+import fp8_reference as R
+import mixture_experts_layer_53_b200 as M
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, F32, E4 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from mixture_experts_layer_53_b200 import build
+    build.build()
+    M.library()
+    assert torch.cuda.is_available()
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def offsets_of(lengths, first=0):
+    return torch.tensor(np.concatenate([[first], first + np.cumsum(lengths)]), dtype=torch.int32, device=DEV)
+
+
+def checked(got, want, bound):
+    """got within bound of want, element by element (NaN never is)."""
+    bad = ~(np.abs(np64(got) - want) <= bound + 1e-300)
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:3].tolist(),
+                           float(np.max(np.abs(np64(got) - want) / np.maximum(bound, 1e-300))))
+
+
+# --------------------------------------------------------------- quantisers
+
+
+def _rows_input(rows, cols, dtype, seed):
+    x = torch.randn((rows, cols), generator=gen(seed), device=DEV)
+    x *= torch.exp(8 * torch.randn((rows, 1), generator=gen(seed + 1), device=DEV))
+    if rows > 2:
+        x[1] = 0                                  # a row of zeros
+        x[2, ::3] *= 1e-30                        # values far below the block's largest
+    if rows > 4:
+        x[3] = 448.0                              # exactly at the largest value
+        x[4] = torch.nextafter(torch.tensor(448.0, device=DEV), torch.tensor(1e9, device=DEV))
+    return x.to(dtype)
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 16), (1, 128), (3, 144), (7, 112), (8, 1024), (9, 1040), (65, 2064), (33, 7168)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_quantize_rows(rows, cols, dtype):
+    x = _rows_input(rows, cols, dtype, rows + cols)
+    q, s = M.moe_quantize_rows(x)
+    wq, ws = R.quantize_rows(np64(x))
+    assert q.dtype == E4 and q.shape == x.shape and s.shape == (-(-cols // 128), rows)
+    assert np.array_equal(np64(s), ws)
+    assert np.array_equal(np64(q), wq)
+
+
+@pytest.mark.parametrize("E,rows,cols", [(1, 16, 16), (2, 128, 128), (3, 144, 400), (2, 1040, 272), (5, 96, 1152)])
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_quantize_weights(E, rows, cols, transpose, dtype):
+    W = torch.randn((E, rows, cols), generator=gen(E + rows), device=DEV)
+    W *= torch.exp(3 * torch.randn((E, rows, 1), generator=gen(5), device=DEV))
+    W[0, :16] = 0
+    W = W.to(dtype)
+    q, s = M.moe_quantize_weights(W, transpose=transpose)
+    wq, ws = R.quantize_weights(np64(W), transpose)
+    assert np.array_equal(np64(s), ws)
+    assert np.array_equal(np64(q), wq)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_blocks_that_are_not_finite(bad, dtype):
+    x = torch.randn((5, 400), generator=gen(1), device=DEV).to(dtype)
+    want, ws = M.moe_quantize_rows(x)
+    x[2, 130] = bad
+    q, s = M.moe_quantize_rows(x)
+    hit = torch.zeros((5, 400), dtype=torch.bool, device=DEV)
+    hit[2, 128:256] = True
+    assert torch.isnan(q.float()[hit]).all() and torch.isnan(s[1, 2])
+    assert torch.equal(q.float()[~hit], want.float()[~hit])
+    s[1, 2] = ws[1, 2]
+    assert torch.equal(s, ws)
+    W = torch.randn((2, 256, 272), generator=gen(2), device=DEV).to(dtype)
+    W[1, 200, 271] = bad
+    for t in (False, True):
+        q, s = M.moe_quantize_weights(W, transpose=t)
+        v = q.float().transpose(1, 2) if t else q.float()
+        v, s = v.cpu(), (s.transpose(1, 2) if t else s).cpu()
+        assert torch.isnan(v[1, 128:, 256:]).all() and torch.isnan(s[1, 1, 2])
+        assert not torch.isnan(v[0]).any() and not torch.isnan(v[1, :128]).any() and not torch.isnan(v[1, :, :256]).any()
+
+
+def test_largest_and_smallest_values():
+    for dtype in (BF, F32):
+        top = torch.finfo(dtype).max
+        tiny = 2.0 ** -133 if dtype == BF else 2.0 ** -149
+        x = torch.tensor([[top] * 16, [tiny] * 16, [0.0] * 16, [-top, tiny] * 8], dtype=dtype, device=DEV)
+        q, s = M.moe_quantize_rows(x)
+        wq, ws = R.quantize_rows(np64(x))
+        assert np.array_equal(np64(q), wq) and np.array_equal(np64(s), ws)
+
+
+def test_empty_rows():
+    q, s = M.moe_quantize_rows(torch.empty((0, 256), dtype=BF, device=DEV))
+    assert q.shape == (0, 256) and s.shape == (2, 0)
+
+
+# ------------------------------------------------------------------ product
+
+
+def _operands(lengths, n, k, seed, first=0, behind=0, free_scales=False):
+    rows, E = first + sum(lengths) + behind, len(lengths)
+    a = M.moe_quantize_rows(torch.randn((rows, k), generator=gen(seed), device=DEV).to(BF))
+    w = M.moe_quantize_weights(torch.randn((E, n, k), generator=gen(seed + 1), device=DEV).mul_(0.05).to(BF))
+    if free_scales:  # a checkpoint's: any fp32 numbers
+        a = a[0], a[1] * torch.exp(torch.randn(a[1].shape, generator=gen(seed + 2), device=DEV))
+        w = w[0], w[1] * torch.exp(torch.randn(w[1].shape, generator=gen(seed + 3), device=DEV))
+    return a, w, offsets_of(lengths, first)
+
+
+def _values(a, w):
+    return R.row_values(np64(a[0]), np64(a[1])), R.weight_values(np64(w[0]), np64(w[1]))
+
+
+PRODUCTS = {
+    "one_row": ([1], 16, 16),
+    "one_row_each": ([1] * 8, 272, 400),
+    "short_k": ([5, 0, 130], 256, 48),
+    "tile_edges": ([128, 129, 127, 0, 256], 384, 256),
+    "odd": ([3, 77, 0, 0, 201, 1], 1040, 720),
+    "long_k": ([2, 0, 40], 144, 4112),
+    "one_expert": ([700], 528, 640),
+    "many_experts": ([i % 5 for i in range(256)], 128, 272),
+    "many_tiles": ([300, 4, 500, 0, 900, 129, 10, 250], 1552, 384),
+}
+
+
+@pytest.mark.parametrize("name", sorted(PRODUCTS))
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("free_scales", [False, True])
+def test_product(name, out, free_scales):
+    lengths, n, k = PRODUCTS[name]
+    a, w, off = _operands(lengths, n, k, seed=len(name), free_scales=free_scales)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    y = M.moe_expert_matmul_fp8(a, off, w, out_dtype=out, status=status)
+    want, bound = R.product(*_values(a, w), off.cpu().numpy())
+    checked(y, want, bound + (R.UBF * (np.abs(want) + bound) if out == BF else 0))
+    assert int(status) == 0
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+def test_rows_outside_every_slice_are_left(out):
+    a, w, off = _operands([10, 0, 150], 144, 272, seed=3, first=7, behind=40)
+    y = torch.full((207, 144), 7.0, dtype=out, device=DEV)
+    M.moe_expert_matmul_fp8(a, off, w, out_dtype=out, out=y)
+    assert (y[:7] == 7).all() and (y[167:] == 7).all()
+    want, bound = R.product(*_values(a, w), off.cpu().numpy())
+    checked(y[7:167], want[7:167], (bound + (R.UBF * (np.abs(want) + bound) if out == BF else 0))[7:167])
+
+
+def test_offsets_are_held_inside_the_rows():
+    a, w, off = _operands([10, 20, 30], 64, 64, seed=4)
+    wild = torch.tensor([-5, 10, 30, 10 ** 9], dtype=torch.int32, device=DEV)
+    assert torch.equal(M.moe_expert_matmul_fp8(a, wild, w), M.moe_expert_matmul_fp8(a, off, w))
+    back = torch.tensor([60, 30, 10, 0], dtype=torch.int32, device=DEV)  # every slice empty
+    y = torch.full((60, 64), 3.0, dtype=BF, device=DEV)
+    M.moe_expert_matmul_fp8(a, back, w, out=y)
+    assert (y == 3).all()
+
+
+def test_no_rows_and_empty_slices():
+    a, w, off = _operands([0, 0, 0], 64, 64, seed=5)
+    assert M.moe_expert_matmul_fp8(a, off, w).shape == (0, 64)
+    a, w, off = _operands([0, 0], 64, 64, seed=5, behind=9)
+    y = torch.full((9, 64), 2.0, dtype=BF, device=DEV)
+    assert (M.moe_expert_matmul_fp8(a, off, w, out=y) == 2).all()
+
+
+def test_a_value_that_is_not_finite_stays_in_its_row():
+    a, w, off = _operands([40, 100], 144, 272, seed=6)
+    clean = M.moe_expert_matmul_fp8(a, off, w, out_dtype=F32)
+    x = torch.randn((140, 272), generator=gen(6), device=DEV).to(BF)
+    x[33, 200] = float("nan")
+    y = M.moe_expert_matmul_fp8(M.moe_quantize_rows(x), off, w, out_dtype=F32)
+    assert torch.isnan(y[33]).all()
+    keep = torch.arange(140, device=DEV) != 33
+    assert torch.equal(y[keep], clean[keep])
+
+
+@pytest.mark.parametrize("lengths,n,k", [([5, 0, 130], 272, 144), ([64] * 4, 1040, 256)])
+def test_input_gradient(lengths, n, k):
+    """dx = dy W by the transposed weights: the formula in 64 bits, and <dy, P v> = <dx, v>: the product is linear in
+    its rows, so this is the difference quotient of <dy, P> in direction v."""
+    g = gen(9)
+    W = torch.randn((len(lengths), n, k), generator=g, device=DEV).mul_(0.05).to(BF)
+    w, wt = M.moe_quantize_weights(W), M.moe_quantize_weights(W, transpose=True)
+    assert torch.equal(w[0].view(torch.uint8).transpose(1, 2), wt[0].view(torch.uint8))
+    off = offsets_of(lengths)
+    rows = sum(lengths)
+    dy = M.moe_quantize_rows(torch.randn((rows, n), generator=g, device=DEV))
+    v = M.moe_quantize_rows(torch.randn((rows, k), generator=g, device=DEV))
+    dx = M.moe_expert_matmul_fp8(dy, off, wt, out_dtype=F32)
+    dyv, Wv = R.row_values(np64(dy[0]), np64(dy[1])), R.weight_values(np64(w[0]), np64(w[1]))
+    want, bound = R.product(dyv, Wv.transpose(0, 2, 1), off.cpu().numpy())
+    checked(dx, want, bound)
+    pv = M.moe_expert_matmul_fp8(v, off, w, out_dtype=F32)
+    vv = R.row_values(np64(v[0]), np64(v[1]))
+    _, pbound = R.product(vv, Wv, off.cpu().numpy())
+    assert abs((dyv * np64(pv)).sum() - (np64(dx) * vv).sum()) <= (np.abs(dyv) * pbound).sum() + (bound * np.abs(vv)).sum()
+
+
+# ---------------------------------------------------------------------- FFN
+
+
+def _weights(E, d, F, act, seed, biases):
+    g = gen(seed)
+    mk = lambda *s: torch.randn(s, generator=g, device=DEV).mul_(0.08).to(BF)  # noqa: E731
+    W = {"W1": mk(E, F, d), "W2": mk(E, d, F), "W3": mk(E, F, d) if act == "swiglu" else None,
+         "b1": mk(E, F) if act == "gelu" and biases else None, "b2": mk(E, d) if biases else None}
+    q = {k: M.moe_quantize_weights(v) if k[0] == "W" and v is not None else v for k, v in W.items()}
+    return W, q
+
+
+def _ffn_reference(q, x, off, act):
+    val = lambda k: R.weight_values(np64(q[k][0]), np64(q[k][1])) if q[k] is not None else None  # noqa: E731
+    vec = lambda k: np64(q[k]) if q[k] is not None else None  # noqa: E731
+    return R.ffn(np64(x), off.cpu().numpy(), val("W1"), val("W2"), act, val("W3"), vec("b1"), vec("b2"))
+
+
+FFNS = {
+    # lengths, d, F, act, biases
+    "token": ([0, 1, 0, 1, 0, 0], 256, 384, "swiglu", False),
+    "token_gelu": ([1], 64, 272, "gelu", True),
+    "few": ([3, 0, 1, 17, 2, 9], 400, 208, "swiglu", True),
+    "narrow": ([40, 33], 16, 16, "swiglu", False),
+    "ragged": ([128, 0, 131, 1, 290], 272, 720, "swiglu", False),
+    "ragged_gelu": ([128, 0, 131, 1, 290], 272, 720, "gelu", True),
+    "gelu_plain": ([77, 200], 144, 144, "gelu", False),
+    "many": ([i % 7 for i in range(200)], 144, 256, "swiglu", False),
+    "wide": ([500, 300], 1040, 1152, "swiglu", True),
+}
+
+
+@pytest.mark.parametrize("name", sorted(FFNS))
+def test_ffn(name):
+    lengths, d, F, act, biases = FFNS[name]
+    _, q = _weights(len(lengths), d, F, act, len(name), biases)
+    rows, off = sum(lengths), offsets_of(lengths)
+    x = torch.randn((rows, d), generator=gen(4), device=DEV).to(BF)
+    cfg = M.make_config(rows, d, F, len(lengths), 1, act=act, dtype="bf16")
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    y = M.moe_expert_ffn_fp8(cfg, x, off, q["W1"], q["W2"], b1=q["b1"], W3=q["W3"], b2=q["b2"], status=status)
+    want, bound = _ffn_reference(q, x, off, act)
+    checked(y, want, bound)
+    # the bound is far below the result's size: a wrong column, scale or row would not pass it
+    assert np.sqrt(np.mean(bound ** 2)) < 0.05 * np.sqrt(np.mean(want ** 2))
+    assert int(status) == 0
+    again = M.moe_expert_ffn_fp8(cfg, x, off, q["W1"], q["W2"], b1=q["b1"], W3=q["W3"], b2=q["b2"])
+    assert torch.equal(y, again)
+
+
+@pytest.mark.parametrize("act", ["swiglu", "gelu"])
+def test_ffn_leaves_rows_outside_every_slice(act):
+    _, q = _weights(3, 144, 272, act, 8, True)
+    off = offsets_of([10, 0, 150], 7)
+    x = torch.randn((207, 144), generator=gen(4), device=DEV).to(BF)
+    x[190] = float("nan")  # a row of no slice holds anything
+    cfg = M.make_config(207, 144, 272, 3, 1, act=act, dtype="bf16")
+    y = torch.full((207, 144), 7.0, dtype=BF, device=DEV)
+    M.moe_expert_ffn_fp8(cfg, x, off, q["W1"], q["W2"], b1=q["b1"], W3=q["W3"], b2=q["b2"], out=y)
+    assert (y[:7] == 7).all() and (y[167:] == 7).all()
+    x[190] = 0
+    want, bound = _ffn_reference(q, x, off, act)
+    checked(y[7:167], want[7:167], bound[7:167])
+
+
+def test_ffn_no_tokens():
+    _, q = _weights(3, 144, 272, "swiglu", 8, False)
+    cfg = M.make_config(0, 144, 272, 3, 2, act="swiglu", dtype="bf16")
+    y = M.moe_expert_ffn_fp8(cfg, torch.empty((0, 144), dtype=BF, device=DEV), offsets_of([0, 0, 0]), q["W1"], q["W2"],
+                             W3=q["W3"])
+    assert y.shape == (0, 144)
+
+
+def test_ffn_captured_and_replayed_beside_an_eager_call():
+    """A captured call and an eager one on another stream, each with its workspace, replayed on new inputs."""
+    lengths = [30, 0, 140, 6]
+    _, q = _weights(4, 256, 384, "swiglu", 3, False)
+    off, rows = offsets_of(lengths), 176
+    cfg = M.make_config(rows, 256, 384, 4, 1, act="swiglu", dtype="bf16")
+    xs = [torch.randn((rows, 256), generator=gen(i), device=DEV).to(BF) for i in range(3)]
+    call = lambda x, **kw: M.moe_expert_ffn_fp8(cfg, x, off, q["W1"], q["W2"], W3=q["W3"], **kw)  # noqa: E731
+    want = [call(x) for x in xs]
+    static, out, ws = xs[0].clone(), torch.empty((rows, 256), dtype=BF, device=DEV), M.moe_expert_ffn_fp8_workspace(cfg)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        call(static, ws=ws, out=out)
+    side = torch.cuda.Stream()
+    for i, x in enumerate(xs):
+        static.copy_(x)
+        side.wait_stream(torch.cuda.current_stream())
+        other = call(xs[i - 1], stream=side)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[i]) and torch.equal(other, want[i - 1])
+
+
+@pytest.mark.parametrize("N,E,k,act,router", [(1, 8, 2, "swiglu", "softmax_topk"), (64, 40, 6, "swiglu", "sigmoid"),
+                                              (333, 6, 2, "gelu", "softmax_topk")])
+def test_layer_on_quantised_experts(N, E, k, act, router):
+    """route -> dispatch -> FFN on 8-bit weights -> combine, as a serving program chains them: every step within its
+    bound of the same chain in 64 bits, and near the bf16 layer."""
+    d, F = 272, 208
+    W, q = _weights(E, d, F, act, 11, False)
+    g = gen(12)
+    x, Wg = torch.randn((N, d), generator=g, device=DEV).to(BF), torch.randn((E, d), generator=g, device=DEV).mul_(0.1).to(BF)
+    cfg = M.make_config(N, d, F, E, k, router=router, act=act, dtype="bf16")
+    ids, w, _ = M.moe_route(cfg, x, Wg)
+    dsp = M.moe_dispatch(cfg, ids, x)
+    ys = M.moe_expert_ffn_fp8(cfg, dsp["x_sorted"], dsp["offsets"], q["W1"], q["W2"], W3=q["W3"])
+    y = M.moe_combine(cfg, ys, w, dsp["inv_perm"])
+    want, bound = _ffn_reference(q, dsp["x_sorted"], dsp["offsets"], act)
+    checked(ys, want, bound)
+    inv = dsp["inv_perm"].cpu().numpy().reshape(N, k)
+    full = (np64(w)[:, :, None] * want[inv]).sum(1)
+    off = (np64(w)[:, :, None] * bound[inv]).sum(1)
+    size = (np64(w)[:, :, None] * (np.abs(want) + bound)[inv]).sum(1)
+    checked(y, full, off + k * R.U32 * size + R.UBF * (np.abs(full) + off + k * R.U32 * size))
+    # Against the bf16 layer: each operand of a product is off by at most 2^-4 of itself and, over a row, by about
+    # 2^-4 / sqrt(3) at random; two operands twice give under 0.1 of the result's norm.
+    ref = M.moe_forward(cfg, x, Wg, W["W1"], W["W2"], W3=W["W3"])["y"]
+    rel = np.linalg.norm(np64(y) - np64(ref)) / np.linalg.norm(np64(ref))
+    assert 1e-4 < rel < 0.1, rel
+
+
+def test_a_side_stream_owns_its_results():
+    """A call given a stream allocates there: its temporaries are not handed to the current stream while it runs."""
+    a, w, off = _operands([300, 200], 528, 640, seed=2)
+    want = M.moe_expert_matmul_fp8(a, off, w)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = [M.moe_expert_matmul_fp8(a, off, w, stream=side) for _ in range(8)]
+    junk = [torch.full((500, 528), float(i), dtype=BF, device=DEV) for i in range(8)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs) and len(junk) == 8
+
+
+def test_refusals_of_the_binding():
+    a, w, off = _operands([4, 4], 64, 64, seed=1)
+    ok = dict(a=a, offsets=off, w=w)
+    for bad, match in [
+        (dict(a=(a[0].float(), a[1])), "a must be"), (dict(a=(a[0], a[1].t().contiguous())), "scales"),
+        (dict(offsets=off.long()), "offsets"), (dict(offsets=off[:2]), "offsets"),
+        (dict(w=(w[0][:, :48].contiguous(), w[1][:, :0].contiguous())), "scales"),
+        (dict(w=(w[0].transpose(1, 2), w[1])), "contiguous"), (dict(out_dtype=torch.float16), "out_dtype"),
+        (dict(out=torch.empty((8, 80), dtype=BF, device=DEV)), "out must be"),
+        (dict(out=torch.empty((8, 64), dtype=F32, device=DEV)), "out must be"),
+        (dict(offsets=off.cpu()), "is on cpu"),
+    ]:
+        with pytest.raises(ValueError, match=match):
+            M.moe_expert_matmul_fp8(**{**ok, **bad})
+    with pytest.raises(M.MoeError, match="UNSUPPORTED"):
+        M.moe_quantize_rows(torch.zeros((4, 24), device=DEV))
+    with pytest.raises(ValueError, match="contiguous"):
+        M.moe_quantize_rows(torch.zeros((64, 64), device=DEV).t()[:, :32])
