@@ -10,14 +10,18 @@
 // in their registers for the whole tile.  Sums inside a block are the tensor
 // core's fp32 accumulation over 128 products, all others fp32 multiply-adds.
 //
-// Warp roles (320 threads, one CTA per SM, persistent over the tile list
+// Warp roles (384 threads, one CTA per SM, persistent over the tile list
 // (expert, n-tile, m-tile), m-tiles innermost so that CTAs that run at the
 // same time share an expert's weight tile through L2):
 //   warp 0      TMA producer: A (16 KB) and W (32 KB) tiles, four stages
 //   warp 1      allocates 512 TMEM columns (two accumulators); one lane
 //               issues the MMAs (M = 128, N = 256, K = 32)
-//   warps 2-9   sums and epilogue: a warp owns 32 rows (its TMEM lane
+//   warps 2, 3  idle (a register split is made by whole warpgroups)
+//   warps 4-11  sums and epilogue: a warp owns 32 rows (its TMEM lane
 //               quarter) and half of the columns, 128 fp32 sums a thread
+// The sums and two 32-column chunks on their way from TMEM need more than
+// the 168 registers that 384 threads launch with: the first warpgroup hands
+// registers over (128 x 56 + 256 x 224 = 384 x 168).
 //
 // SwiGLU: the W tile holds 128 rows of W1 and the same 128 rows of W3; a
 // thread holds the gate and the up columns of 64 hidden units.  The 128
@@ -45,7 +49,10 @@ constexpr int A_BYTES = BM * BK;
 constexpr int W_BYTES = BN * BK;
 constexpr int STAGE_BYTES = A_BYTES + W_BYTES;
 constexpr int SUM_WARPS = 8;
-constexpr int THREADS = 64 + 32 * SUM_WARPS;
+constexpr int FIRST_SUM_WARP = 4;
+constexpr int THREADS = 32 * (FIRST_SUM_WARP + SUM_WARPS);
+constexpr int LAUNCH_REGS = 168, ROLE_REGS = 56, SUM_REGS = 224;
+static_assert(32 * FIRST_SUM_WARP * ROLE_REGS + 32 * SUM_WARPS * SUM_REGS <= THREADS * LAUNCH_REGS, "register split");
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int CHUNK_BYTES = 32 * 64;  // a warp's staging: 32 rows of 64 bytes
 
@@ -144,6 +151,18 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
     return d;
 }
 
+// Until this thread's TMEM loads have landed; r ties the uses of the loaded
+// values to this point.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+
 // 64 values of a thread's row from column c on, as e4m3.
 __device__ __forceinline__ void store_h64(const float (&h)[64], float inv, uint8_t *row, int c, int n_out)
 {
@@ -184,6 +203,13 @@ __device__ __forceinline__ void store_chunk(const uint4 (&p)[4], uint8_t *stage,
         if (row_first + r < row_end && byte0 + j * 16 < byte_end)
             st16(out + (row_first + r) * row_bytes + byte0 + j * 16, v);
     }
+}
+
+// First accumulator column of a thread's chunk c of 32: SwiGLU, 64 gate and
+// then 64 up columns; else 128 consecutive ones.
+template <int EPI> __device__ __forceinline__ uint32_t chunk_col(int c, int half)
+{
+    return EPI == EPI_SWIGLU ? (c >> 1) * 128 + half * 64 + (c & 1) * 32 : half * 128 + c * 32;
 }
 
 template <int EPI>
@@ -254,8 +280,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int total = ctl->mt[g.E] * g.n_tiles;
     const int num_kb = (g.K + BK - 1) / BK;
 
-    if (warp == 0) {
-        if (lane == 0) {
+    if (warp < FIRST_SUM_WARP) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(ROLE_REGS));
+        if (warp == 0 && lane == 0) {
             // ------------------------------------------------ TMA producer
             int stage = 0;
             uint32_t phase = 0, armed = 0, armed_parity = 0;
@@ -290,9 +317,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if ((armed >> s) & 1u)
                         mbar_wait(&ctl->full[s], (armed_parity >> s) & 1u, abort_flag, g.status, false);
             }
-        }
-    } else if (warp == 1) {
-        if (lane == 0) {
+        } else if (warp == 1 && lane == 0) {
             // -------------------------------------------------- MMA issuer
             constexpr uint32_t idesc = idesc_f8(BM, BN);
             int stage = 0, buf = 0;
@@ -332,9 +357,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SUM_REGS));
         // ---------------------------------------------- sums and epilogue
-        const int quarter = warp & 3, half = (warp - 2) >> 2;
-        uint8_t *stage = ctl->stage[warp - 2];
+        const int quarter = warp & 3, half = (warp - FIRST_SUM_WARP) >> 2;
+        uint8_t *stage = ctl->stage[warp - FIRST_SUM_WARP];
         const int nblocks = (g.n_out + kFp8Block - 1) / kFp8Block;
         int buf = 0;
         uint32_t tphase = 0, xphase = 0;
@@ -373,16 +399,18 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (active) {
                     const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                                            static_cast<uint32_t>(buf * BN);
+                    // 32 columns at a time, the next ones on their way
+                    // while these are added
+                    uint32_t r[2][32];
+                    tmem_ld32(tbase + chunk_col<EPI>(0, half), r[0]);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        uint32_t r[32];
-                        const int col = EPI == EPI_SWIGLU ? (c >> 1) * 128 + half * 64 + (c & 1) * 32 : half * 128 + c * 32;
-                        tmem_ld32(tbase + static_cast<uint32_t>(col), r);
-                        tmem_ld_wait();
+                        tmem_ld_wait(r[c & 1]);
+                        if (c < 3) tmem_ld32(tbase + chunk_col<EPI>(c + 1, half), r[(c + 1) & 1]);
                         const uint64_t p = (EPI == EPI_SWIGLU && c >= 2) ? p3 : p1;
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            acc[c * 16 + i] = fma2(pack2(r[2 * i], r[2 * i + 1]), p, acc[c * 16 + i]);
+                            acc[c * 16 + i] = fma2(pack2(r[c & 1][2 * i], r[c & 1][2 * i + 1]), p, acc[c * 16 + i]);
                     }
                 }
                 tc_fence_before();
