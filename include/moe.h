@@ -453,7 +453,12 @@ MOE_API moe_status moe_permute_rows(int32_t dtype, const void *src, const int32_
  * the smallest power of two s (at least 2^-126) with max |x| <= 448 s, so
  * x / s is exact and the only rounding is e4m3's, to nearest even; a block
  * that holds a NaN or an infinity gets a NaN scale and NaN values.  The
- * products take any fp32 scales (a checkpoint's, for instance).
+ * products apply powers of two (or NaN) inside the tensor core; any_scales =
+ * 1 takes every fp32 scale (a checkpoint's, for instance) and applies it on
+ * the CUDA cores, which costs up to twice the time where the product is
+ * bound by arithmetic.  With any_scales = 0 a scale that is no positive normal
+ * power of two is taken for the one below it and sets MOE_ERR_INVALID_ARG in
+ * dev_status.
  * Layouts, row-major and contiguous:
  *   activations  q [rows, cols] e4m3,    scales [ceil(cols/128), rows] f32
  *   weights      q [E, rows, cols] e4m3, scales [E, ceil(rows/128), ceil(cols/128)] f32
@@ -482,16 +487,17 @@ MOE_API moe_status moe_quantize_weights(int32_t dtype, const void *W, int32_t E,
  * as above, out [rows, n] in out_dtype (MOE_F32 or MOE_BF16).  Products and
  * sums in fp32, rounded once at the end.  offsets [E+1] is read on the device
  * and held inside 0 .. rows; rows outside every slice are left as they were.
- * E <= 256.  dev_status (may be NULL): MOE_ERR_TIMEOUT.  No workspace.
+ * E <= 256.  dev_status (may be NULL): MOE_ERR_TIMEOUT, MOE_ERR_INVALID_ARG
+ * (scales, above).  No workspace.
  */
 MOE_API moe_status moe_expert_matmul_fp8(int64_t rows, int32_t n, int32_t k, int32_t E, const void *a_q,
                                          const float *a_scales, const int32_t *offsets, const void *w_q,
-                                         const float *w_scales, int32_t out_dtype, void *out,
-                                         int32_t *dev_status, moe_stream_t stream);
+                                         const float *w_scales, int32_t any_scales, int32_t out_dtype,
+                                         void *out, int32_t *dev_status, moe_stream_t stream);
 
 /* Quantised expert weights of moe_expert_ffn_fp8, shapes as W1, W3, W2, b1
  * and b2 above; the biases are bf16 and may be NULL, W3 and its scales are
- * SwiGLU only, b1 GELU only. */
+ * SwiGLU only, b1 GELU only.  any_scales: as for moe_expert_matmul_fp8. */
 typedef struct {
     const void *W1;
     const float *W1_scales;
@@ -501,6 +507,7 @@ typedef struct {
     const float *W2_scales;
     const void *b1;
     const void *b2;
+    int32_t any_scales;
 } moe_fp8_experts;
 
 /* Workspace bytes moe_expert_ffn_fp8 needs for cfg (0 if it does not accept cfg). */

@@ -77,7 +77,7 @@ class MoeGrads(ctypes.Structure):
 class Fp8Experts(ctypes.Structure):
     """Mirror of ``moe_fp8_experts`` in include/moe.h (device pointers)."""
     _fields_ = [(name, ctypes.c_void_p) for name in
-                ("W1", "W1_scales", "W3", "W3_scales", "W2", "W2_scales", "b1", "b2")]
+                ("W1", "W1_scales", "W3", "W3_scales", "W2", "W2_scales", "b1", "b2")] + [("any_scales", ctypes.c_int32)]
 
 
 class MoeError(RuntimeError):
@@ -153,7 +153,7 @@ def library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.moe_quantize_rows.restype = st
     lib.moe_quantize_weights.argtypes = [i32, vp, i32, i32, i32, i32, vp, f32p, vp]
     lib.moe_quantize_weights.restype = st
-    lib.moe_expert_matmul_fp8.argtypes = [i64, i32, i32, i32, vp, f32p, i32p, vp, f32p, i32, vp, i32p, vp]
+    lib.moe_expert_matmul_fp8.argtypes = [i64, i32, i32, i32, vp, f32p, i32p, vp, f32p, i32, i32, vp, i32p, vp]
     lib.moe_expert_matmul_fp8.restype = st
     lib.moe_expert_ffn_fp8_workspace_size.argtypes = [cfgp]
     lib.moe_expert_ffn_fp8_workspace_size.restype = sz
@@ -492,12 +492,13 @@ def moe_quantize_weights(W: torch.Tensor, transpose: bool = False, stream=None) 
 
 def moe_expert_matmul_fp8(a: Tuple[torch.Tensor, torch.Tensor], offsets: torch.Tensor,
                           w: Tuple[torch.Tensor, torch.Tensor], out_dtype: torch.dtype = torch.bfloat16,
-                          out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
-                          stream=None) -> torch.Tensor:
+                          out: Optional[torch.Tensor] = None, any_scales: bool = False,
+                          status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Rows offsets[e] .. offsets[e+1]-1 of a times w[e]^T -> [rows, n] (bf16 or f32).
 
-    a = (q [rows, k], scales) from moe_quantize_rows, w = (q [E, n, k], scales) from moe_quantize_weights
-    (or any fp32 scales).  Rows outside every slice keep what ``out`` held."""
+    a = (q [rows, k], scales) from moe_quantize_rows, w = (q [E, n, k], scales) from moe_quantize_weights.
+    Scales are powers of two (others set status to 1); any_scales=True takes every fp32 scale, more slowly.
+    Rows outside every slice keep what ``out`` held."""
     where = "moe_expert_matmul_fp8"
     (aq, asc), (wq, wsc) = a, w
     if aq.dim() != 2 or wq.dim() != 3:
@@ -512,7 +513,8 @@ def moe_expert_matmul_fp8(a: Tuple[torch.Tensor, torch.Tensor], offsets: torch.T
             rows, n, k, E, _arg(where, "a", aq, e4m3, (rows, k), dev),
             _arg(where, "a's scales", asc, f32, (kb, rows), dev),
             _arg(where, "offsets", offsets, torch.int32, (E + 1,), dev), _arg(where, "w", wq, e4m3, (E, n, k), dev),
-            _arg(where, "w's scales", wsc, f32, (E, _fp8_blocks(n), kb), dev), int(out_dtype == torch.bfloat16),
+            _arg(where, "w's scales", wsc, f32, (E, _fp8_blocks(n), kb), dev), int(bool(any_scales)),
+            int(out_dtype == torch.bfloat16),
             _arg(where, "out", out, out_dtype, (rows, n), dev),
             _arg(where, "status", status, torch.int32, (1,), dev) if status is not None else None, _stream())
     _check(rc, where)
@@ -532,9 +534,10 @@ def moe_expert_ffn_fp8(cfg: MoeConfig, x_sorted: torch.Tensor, offsets: torch.Te
                        b1: Optional[torch.Tensor] = None, W3: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
                        b2: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
                        status: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
-                       stream=None) -> torch.Tensor:
+                       any_scales: bool = False, stream=None) -> torch.Tensor:
     """moe_expert_ffn on quantised weights: W1, W2 (and W3) are (q, scales) pairs of moe_quantize_weights, x_sorted
-    and the result bf16.  Rows outside every slice keep what ``out`` held."""
+    and the result bf16.  any_scales as for moe_expert_matmul_fp8.  Rows outside every slice keep what ``out``
+    held."""
     where, dev = "moe_expert_ffn_fp8", x_sorted.device
     e4m3, f32, bf16 = torch.float8_e4m3fn, torch.float32, torch.bfloat16
     E, d, F, A = cfg.E, cfg.d_model, cfg.d_ff, cfg.N * cfg.k
@@ -552,7 +555,7 @@ def moe_expert_ffn_fp8(cfg: MoeConfig, x_sorted: torch.Tensor, offsets: torch.Te
         ws = ws if ws is not None else moe_expert_ffn_fp8_workspace(cfg, dev)
         out = out if out is not None else torch.empty((A, d), dtype=bf16, device=dev)
         w = Fp8Experts(*pair("W1", W1, F, d), *pair("W3", W3, F, d), *pair("W2", W2, d, F),
-                       one("b1", b1, bf16, (E, F)), one("b2", b2, bf16, (E, d)))
+                       one("b1", b1, bf16, (E, F)), one("b2", b2, bf16, (E, d)), int(bool(any_scales)))
         rc = library().moe_expert_ffn_fp8(
             ctypes.byref(cfg), _arg(where, "x_sorted", x_sorted, bf16, (A, d), dev),
             _arg(where, "offsets", offsets, torch.int32, (E + 1,), dev), ctypes.byref(w),

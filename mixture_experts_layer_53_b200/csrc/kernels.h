@@ -361,7 +361,10 @@ struct Fp8GemmArgs {
     int64_t rows;
     int E, n, k;
 };
+// any scales (gemm_fp8_sm100.cu), and scales that are powers of two
+// (gemm_mxfp8_sm100.cu: other values are reported in *status)
 cudaError_t launch_gemm_fp8(const Fp8GemmArgs &a, int num_sms, cudaStream_t s);
+cudaError_t launch_gemm_mxfp8(const Fp8GemmArgs &a, int num_sms, cudaStream_t s);
 
 // ---- balance loss over sequences (balance.cu)
 struct BalanceArgs {

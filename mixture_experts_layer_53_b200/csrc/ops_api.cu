@@ -32,6 +32,13 @@ template <typename F> moe_status guarded(F &&f)
 
 moe_status done(cudaError_t err) { return err == cudaSuccess ? MOE_OK : record_cuda_error(err); }
 
+// Scales that are powers of two are applied by the tensor core, others on
+// the CUDA cores.
+cudaError_t product(int32_t any_scales, const Fp8GemmArgs &g, cudaStream_t s)
+{
+    return any_scales ? launch_gemm_fp8(g, device_sms(), s) : launch_gemm_mxfp8(g, device_sms(), s);
+}
+
 size_t align256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 
 struct FfnLayout {
@@ -100,12 +107,12 @@ moe_status moe_quantize_weights(int32_t dtype, const void *W, int32_t E, int32_t
 
 moe_status moe_expert_matmul_fp8(int64_t rows, int32_t n, int32_t k, int32_t E, const void *a_q,
                                  const float *a_scales, const int32_t *offsets, const void *w_q,
-                                 const float *w_scales, int32_t out_dtype, void *out, int32_t *dev_status,
-                                 moe_stream_t stream)
+                                 const float *w_scales, int32_t any_scales, int32_t out_dtype, void *out,
+                                 int32_t *dev_status, moe_stream_t stream)
 {
     return guarded([&] {
         if (out_dtype != MOE_F32 && out_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
-        if (rows < 0 || n <= 0 || k <= 0 || E <= 0) return MOE_ERR_INVALID_ARG;
+        if (rows < 0 || n <= 0 || k <= 0 || E <= 0 || (any_scales != 0 && any_scales != 1)) return MOE_ERR_INVALID_ARG;
         if (E > kMaxE || n % 16 != 0 || k % 16 != 0 || rows >= kMaxRows) return MOE_ERR_UNSUPPORTED;
         if (!offsets || !given(w_q) || !given(w_scales)) return MOE_ERR_INVALID_ARG;
         if (rows == 0) return MOE_OK;
@@ -123,7 +130,7 @@ moe_status moe_expert_matmul_fp8(int64_t rows, int32_t n, int32_t k, int32_t E, 
         g.E = E;
         g.n = n;
         g.k = k;
-        return done(launch_gemm_fp8(g, device_sms(), reinterpret_cast<cudaStream_t>(stream)));
+        return done(product(any_scales, g, reinterpret_cast<cudaStream_t>(stream)));
     });
 }
 
@@ -145,6 +152,7 @@ moe_status moe_expert_ffn_fp8(const moe_config *cfg, const void *x_sorted, const
         if (!given(w->W1) || !given(w->W1_scales) || !given(w->W2) || !given(w->W2_scales)) return MOE_ERR_INVALID_ARG;
         if (swiglu ? (!given(w->W3) || !given(w->W3_scales) || w->b1) : (w->W3 || w->W3_scales)) return MOE_ERR_INVALID_ARG;
         if (!aligned16(w->b1) || !aligned16(w->b2)) return MOE_ERR_INVALID_ARG;
+        if (w->any_scales != 0 && w->any_scales != 1) return MOE_ERR_INVALID_ARG;
         const FfnLayout L = ffn_layout(cfg);
         if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 || ws_bytes < L.total) return MOE_ERR_WORKSPACE;
         if (cfg->N == 0) return MOE_OK;
@@ -152,7 +160,6 @@ moe_status moe_expert_ffn_fp8(const moe_config *cfg, const void *x_sorted, const
         uint8_t *base = static_cast<uint8_t *>(ws);
         float *xs = reinterpret_cast<float *>(base + L.xs), *hs = reinterpret_cast<float *>(base + L.hs);
         const int64_t rows = cfg->N * cfg->k;
-        const int sms = device_sms();
         cudaError_t err = launch_quantize_rows(kBF16, x_sorted, rows, cfg->d_model, base + L.xq, xs, s);
         if (err != cudaSuccess) return record_cuda_error(err);
         Fp8GemmArgs g{};
@@ -172,7 +179,7 @@ moe_status moe_expert_ffn_fp8(const moe_config *cfg, const void *x_sorted, const
         g.E = cfg->E;
         g.n = cfg->d_ff;
         g.k = cfg->d_model;
-        if ((err = launch_gemm_fp8(g, sms, s)) != cudaSuccess) return record_cuda_error(err);
+        if ((err = product(w->any_scales, g, s)) != cudaSuccess) return record_cuda_error(err);
         g.epi = kFp8Bf16;
         g.a = base + L.hq;
         g.a_scales = hs;
@@ -185,7 +192,7 @@ moe_status moe_expert_ffn_fp8(const moe_config *cfg, const void *x_sorted, const
         g.h_scales = nullptr;
         g.n = cfg->d_model;
         g.k = cfg->d_ff;
-        return done(launch_gemm_fp8(g, sms, s));
+        return done(product(w->any_scales, g, s));
     });
 }
 

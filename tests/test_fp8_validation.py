@@ -44,12 +44,12 @@ def test_quantize_weights(lib, args, code):
 
 @pytest.mark.parametrize("change,code", [
     (dict(rows=-1), 1), (dict(n=0), 1), (dict(k=0), 1), (dict(E=0), 1), (dict(E=257), 2), (dict(n=40), 2),
-    (dict(k=40), 2), (dict(rows=2 ** 31), 2), (dict(dt=2), 1), (dict(a=None), 1), (dict(a=OFF), 1), (dict(asc=None), 1),
+    (dict(k=40), 2), (dict(rows=2 ** 31), 2), (dict(dt=2), 1), (dict(any=2), 1), (dict(a=None), 1), (dict(a=OFF), 1), (dict(asc=None), 1),
     (dict(off=None), 1), (dict(w=OFF), 1), (dict(wsc=None), 1), (dict(out=None), 1), (dict(out=OFF), 1),
     (dict(rows=0, a=None, asc=None, out=None), 0),
 ])
 def test_matmul(lib, change, code):
-    a = dict(rows=4, n=64, k=64, E=2, a=A, asc=A, off=A, w=A, wsc=A, dt=1, out=A)
+    a = dict(rows=4, n=64, k=64, E=2, a=A, asc=A, off=A, w=A, wsc=A, any=0, dt=1, out=A)
     a.update(change)
     assert lib.moe_expert_matmul_fp8(*a.values(), None, None) == code
 
@@ -68,7 +68,7 @@ def test_ffn(lib):
         assert call(cfg(), w(**{name: None})) == 1 and call(cfg(), w(**{name: 0x10008})) == 1
     assert call(cfg(), w(b1=0x10000)) == 1                    # a hidden bias with SwiGLU
     assert call(cfg(act="gelu"), w()) == 1                    # W3 with GELU
-    assert call(cfg(), w(b2=0x10008)) == 1
+    assert call(cfg(), w(b2=0x10008)) == 1 and call(cfg(), w(any_scales=-1)) == 1
     assert call(cfg(), None) == 1 and call(cfg(), w(), x=None) == 1 and call(cfg(), w(), off=None) == 1
     assert call(cfg(), w(), y=OFF) == 1
     assert call(cfg(), w(), ws=None) == 4 and call(cfg(), w(), ws=OFF) == 4

@@ -145,6 +145,7 @@ PRODUCTS = {
     "long_k": ([2, 0, 40], 144, 4112),
     "one_expert": ([700], 528, 640),
     "many_experts": ([i % 5 for i in range(256)], 128, 272),
+    "pairs": ([256, 255, 257, 1000], 1040, 720),
     "many_tiles": ([300, 4, 500, 0, 900, 129, 10, 250], 1552, 384),
 }
 
@@ -156,20 +157,52 @@ def test_product(name, out, free_scales):
     lengths, n, k = PRODUCTS[name]
     a, w, off = _operands(lengths, n, k, seed=len(name), free_scales=free_scales)
     status = torch.zeros(1, dtype=torch.int32, device=DEV)
-    y = M.moe_expert_matmul_fp8(a, off, w, out_dtype=out, status=status)
+    y = M.moe_expert_matmul_fp8(a, off, w, out_dtype=out, any_scales=free_scales, status=status)
     want, bound = R.product(*_values(a, w), off.cpu().numpy())
     checked(y, want, bound + (R.UBF * (np.abs(want) + bound) if out == BF else 0))
     assert int(status) == 0
 
 
 @pytest.mark.parametrize("out", [BF, F32])
-def test_rows_outside_every_slice_are_left(out):
+@pytest.mark.parametrize("free_scales", [False, True])
+def test_rows_outside_every_slice_are_left(out, free_scales):
     a, w, off = _operands([10, 0, 150], 144, 272, seed=3, first=7, behind=40)
     y = torch.full((207, 144), 7.0, dtype=out, device=DEV)
-    M.moe_expert_matmul_fp8(a, off, w, out_dtype=out, out=y)
+    M.moe_expert_matmul_fp8(a, off, w, out_dtype=out, out=y, any_scales=free_scales)
     assert (y[:7] == 7).all() and (y[167:] == 7).all()
     want, bound = R.product(*_values(a, w), off.cpu().numpy())
     checked(y[7:167], want[7:167], (bound + (R.UBF * (np.abs(want) + bound) if out == BF else 0))[7:167])
+
+
+def test_scales_of_many_sizes():
+    """Powers of two over 2^-100 .. 2^20 that differ from block to block and row to row, products near 1."""
+    a, w, off = _operands([200, 9, 330], 400, 1168, seed=21)
+    e = torch.randint(-100, 20, (1, a[1].shape[1]), generator=gen(1), device=DEV)
+    f = torch.randint(-6, 6, a[1].shape, generator=gen(2), device=DEV)
+    a = a[0], a[1] * torch.exp2((e + f).float())
+    w = w[0], w[1] * torch.exp2(torch.randint(-8, 8, w[1].shape, generator=gen(3), device=DEV).float())
+    want, bound = R.product(*_values(a, w), off.cpu().numpy())
+    for free in (False, True):
+        checked(M.moe_expert_matmul_fp8(a, off, w, out_dtype=F32, any_scales=free), want, bound)
+
+
+def test_scales_that_are_no_powers_of_two_are_reported():
+    a, w, off = _operands([20, 30], 64, 272, seed=5)
+    for scales, at in ((a[1], (1, 45)), (w[1], (1, 0, 2))):
+        for bad in (1.5, 0.0, -1.0, 1e-40):
+            keep = float(scales[at])
+            scales[at] = bad
+            status = torch.zeros(1, dtype=torch.int32, device=DEV)
+            M.moe_expert_matmul_fp8(a, off, w, status=status)
+            assert int(status) == 1
+            M.moe_expert_matmul_fp8(a, off, w, any_scales=True, status=status.zero_())
+            assert int(status) == 0
+            scales[at] = keep
+    short = torch.tensor([0, 20, 40], dtype=torch.int32, device=DEV)
+    a[1][0, 45] = 3.0  # a row of no slice
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    M.moe_expert_matmul_fp8(a, short, w, status=status)
+    assert int(status) == 0
 
 
 def test_offsets_are_held_inside_the_rows():
@@ -266,6 +299,8 @@ def test_ffn(name):
     y = M.moe_expert_ffn_fp8(cfg, x, off, q["W1"], q["W2"], b1=q["b1"], W3=q["W3"], b2=q["b2"], status=status)
     want, bound = _ffn_reference(q, x, off, act)
     checked(y, want, bound)
+    checked(M.moe_expert_ffn_fp8(cfg, x, off, q["W1"], q["W2"], b1=q["b1"], W3=q["W3"], b2=q["b2"], any_scales=True),
+            want, bound)
     # the bound is far below the result's size: a wrong column, scale or row would not pass it
     assert np.sqrt(np.mean(bound ** 2)) < 0.05 * np.sqrt(np.mean(want ** 2))
     assert int(status) == 0
