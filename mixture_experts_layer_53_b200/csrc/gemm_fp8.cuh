@@ -23,11 +23,7 @@ constexpr int BK = kFp8Block;    // a k-block: one scale block, one 128-byte swi
 constexpr int SUM_WARPS = 8;     // epilogue warps: lane quarter x column half
 constexpr int FIRST_SUM_WARP = 4;
 constexpr int THREADS = 32 * (FIRST_SUM_WARP + SUM_WARPS);
-// The epilogue holds up to 128 values and two 32-column chunks on their way
-// from TMEM: more than the 168 registers that 384 threads launch with.  The
-// first warpgroup hands registers over.
-constexpr int LAUNCH_REGS = 168, ROLE_REGS = 56, SUM_REGS = 224;
-static_assert(32 * FIRST_SUM_WARP * ROLE_REGS + 32 * SUM_WARPS * SUM_REGS <= THREADS * LAUNCH_REGS, "register split");
+constexpr int LAUNCH_REGS = 168;  // a thread of 384 launches with
 constexpr int CHUNK_BYTES = 32 * 64;  // a warp's staging: 32 rows of 64 bytes
 
 struct GemmArgs {

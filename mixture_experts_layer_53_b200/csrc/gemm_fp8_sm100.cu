@@ -37,6 +37,8 @@ namespace {
 using namespace fp8;
 
 constexpr int STAGES = 4;
+constexpr int ROLE_REGS = 56, SUM_REGS = 224;
+static_assert(32 * FIRST_SUM_WARP * ROLE_REGS + 32 * SUM_WARPS * SUM_REGS <= THREADS * LAUNCH_REGS, "register split");
 constexpr int A_BYTES = BM * BK;
 constexpr int W_BYTES = BN * BK;
 constexpr int STAGE_BYTES = A_BYTES + W_BYTES;

@@ -24,7 +24,8 @@
 //               to a k-block
 //   warps 2, 3  scales: pack four k-blocks' exponents into a word per row,
 //               in the [row % 32][row / 32] order that tcgen05.cp spreads
-//               over the TMEM lanes; alternate groups of four k-blocks
+//               over the TMEM lanes; alternate groups of four k-blocks,
+//               the next group's scales on their way while one is packed
 //   warps 4-11  epilogue: a warp owns 32 rows (its TMEM lane quarter) and
 //               half of the columns
 //
@@ -44,11 +45,17 @@ namespace {
 
 using namespace fp8;
 
+// The epilogue holds a thread's 128 accumulator values, more than the 168
+// registers that 384 threads launch with have room for beside the rest: the
+// first warpgroup hands registers over (128 x 88 + 256 x 208 = 384 x 168).
+constexpr int ROLE_REGS = 88, SUM_REGS = 208;
+static_assert(32 * FIRST_SUM_WARP * ROLE_REGS + 32 * SUM_WARPS * SUM_REGS <= THREADS * LAUNCH_REGS, "register split");
 constexpr int GROUP = 4;                     // k-blocks of one scale word
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t ACC_STEP = 232;           // second accumulator's first column
 constexpr uint32_t SCALE_COL = 488;          // + 12 per group slot: 4 of A, 8 of W
 constexpr int SCALE_BYTES = 3 * 512;         // A's 128 rows, W's 256
+constexpr int SLOTS = 4;                     // groups of scales in shared memory
 constexpr int A_BYTES = BM * BK;
 
 template <bool PAIR> constexpr int w_bytes() { return (PAIR ? BN / 2 : BN) * BK; }
@@ -57,14 +64,14 @@ template <bool PAIR> constexpr int stages() { return PAIR ? 6 : 4; }
 
 template <bool PAIR> struct Ctl {
     alignas(1024) uint8_t stage[SUM_WARPS][CHUNK_BYTES];
-    alignas(128) uint8_t scales[2][SCALE_BYTES];
+    alignas(128) uint8_t scales[SLOTS][SCALE_BYTES];
     Exchange exchange;
     // a pair's barriers: full, sfull, tempty and shared_free are the even
     // CTA's (both CTAs' arrivals); empty, sempty, tfull are signalled in both
     uint64_t full[stages<PAIR>()];
     uint64_t empty[stages<PAIR>()];
-    uint64_t sfull[2];
-    uint64_t sempty[2];
+    uint64_t sfull[SLOTS];
+    uint64_t sempty[SLOTS];
     uint64_t tfull[2];
     uint64_t tempty[2];
     uint64_t shared_free;
@@ -127,6 +134,14 @@ __device__ __forceinline__ uint64_t desc_scales(uint32_t smem_addr)
     return d;
 }
 
+// A load that stays where it is written: ahead of its use by a group.
+__device__ __forceinline__ float load_ahead(const float *p)
+{
+    float v;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+
 template <bool PAIR> __device__ __forceinline__ void commit(uint64_t *bar)
 {
     if constexpr (PAIR) umma_commit_pair(bar, 0x3);
@@ -154,10 +169,12 @@ __device__ __forceinline__ void
             mbar_init(&ctl->empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(&ctl->sfull[b], CTAS);
-            mbar_init(&ctl->sempty[b], 1);
             mbar_init(&ctl->tfull[b], 1);
             mbar_init(&ctl->tempty[b], SUM_WARPS * CTAS);
+        }
+        for (int s = 0; s < SLOTS; ++s) {
+            mbar_init(&ctl->sfull[s], CTAS);
+            mbar_init(&ctl->sempty[s], 1);
         }
         for (int q = 0; q < 4; ++q) mbar_init(&ctl->exchange.there[q], 2);
         mbar_init(&ctl->shared_free, SUM_WARPS * CTAS);
@@ -241,8 +258,8 @@ __device__ __forceinline__ void
             }
         } else if (warp == 1 && lane == 0 && leader) {
             // -------------------------------------------------- MMA issuer
-            int stage = 0, buf = 0, slot = 0;
-            uint32_t phase = 0, sphase = 0, tphase = 0, shared_phase = 1;
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, tphase = 0, shared_phase = 1, group = 0;
             bool ok = true, issued = false;
             for (int t = first; t < total && ok; t += step) {
                 // this accumulator's last tile has been read, and of the
@@ -254,14 +271,18 @@ __device__ __forceinline__ void
                 tc_fence_after();
                 const uint32_t d = tmem_base + (buf ? ACC_STEP : 0u);
                 for (int kb0 = 0; kb0 < num_kb && ok; kb0 += GROUP) {
-                    // the slot's scales are there, so the MMAs that read its
-                    // TMEM columns last are done (the scale warp waited)
-                    if (!mbar_wait<PAIR>(&ctl->sfull[slot], sphase, abort_flag, g.status)) {
+                    // The group's scales are there, and the MMAs of the
+                    // group before the last, which read the same TMEM
+                    // columns, are done.
+                    const uint32_t slot = group % SLOTS, last = (group - 2) % SLOTS;
+                    if (!mbar_wait<PAIR>(&ctl->sfull[slot], group / SLOTS & 1u, abort_flag, g.status) ||
+                        (group >= 2 &&
+                         !mbar_wait(&ctl->sempty[last], (group - 2) / SLOTS & 1u, abort_flag, g.status))) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sa = tmem_base + SCALE_COL + static_cast<uint32_t>(slot) * 12u, sb = sa + 4u;
+                    const uint32_t sa = tmem_base + SCALE_COL + (group & 1u) * 12u, sb = sa + 4u;
                     const uint32_t src = smem_u32(ctl->scales[slot]);
                     copy_scales<PAIR>(sa, desc_scales(src));
                     copy_scales<PAIR>(sb, desc_scales(src + 512));
@@ -289,8 +310,7 @@ __device__ __forceinline__ void
                     }
                     if (!ok) break;
                     commit<PAIR>(&ctl->sempty[slot]);
-                    slot ^= 1;
-                    if (slot == 0) sphase ^= 1u;
+                    ++group;
                 }
                 if (!ok) break;
                 commit<PAIR>(&ctl->tfull[buf]);
@@ -305,64 +325,90 @@ __device__ __forceinline__ void
             }
         } else if (warp >= 2) {
             // ------------------------------------------------------ scales
-            const int mine = warp - 2;  // groups of this parity, and their slot
-            const uint32_t sfull = PAIR ? mapa_shared(smem_u32(&ctl->sfull[mine]), 0) : smem_u32(&ctl->sfull[mine]);
             const int nblocks = (g.n_out + kFp8Block - 1) / kFp8Block;
-            uint32_t phase = 1;
-            int count = 0;
-            bool ok = true, odd_scale = false;
-            for (int t = first; t < total && ok; t += step) {
-                const Tile ti = decode_tile(t, sl, g.E, g.n_tiles);
-                const int64_t row0 = sl->off[ti.e] + static_cast<int64_t>(ti.m_tile) * TILE_M + rank * BM;
-                const int64_t row_end = sl->end[ti.e];
-                for (int kb0 = 0; kb0 < num_kb; kb0 += GROUP) {
-                    if ((count++ & 1) != mine) continue;
-                    // exponent codes; a scale that is no power of two (zero,
-                    // negative, any mantissa) is reported
-                    auto code = [&](float s, bool counts) {
-                        const uint32_t b = __float_as_uint(s), e = b >> 23;
-                        odd_scale |= counts && (e == 0 || e > 255 || (e < 255 && (b & 0x7FFFFFu) != 0));
-                        return e & 255u;
-                    };
-                    uint32_t w[4];  // rows lane, lane + 32, ...
+            const int groups = (num_kb + GROUP - 1) / GROUP;
+            bool odd_scale = false;
+            // a group of k-blocks and its values on their way from memory
+            struct Fetch {
+                int t, gi;        // tile, group of the tile
+                float a[4][GROUP];  // rows lane, lane + 32, ... of four k-blocks
+                float w;          // lanes 0-3, 4-7: the two 128-column halves of W
+                uint32_t rows;    // bit i: row i of this lane is in the slice
+            };
+            Tile ti{};
+            int decoded = -1;
+            auto fetch = [&](Fetch &f) {
+                if (f.t >= total) return;
+                if (decoded != f.t) ti = decode_tile(f.t, sl, g.E, g.n_tiles);
+                decoded = f.t;
+                const int kb0 = f.gi * GROUP;
+                const int64_t row0 = sl->off[ti.e] + static_cast<int64_t>(ti.m_tile) * TILE_M + rank * BM + lane;
+                f.rows = 0;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int64_t row = row0 + 32 * i + lane;
-                        const float *p = g.a_scales + min64(row, g.rows - 1) + static_cast<int64_t>(kb0) * g.rows;
-                        w[i] = 0;
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t row = row0 + 32 * i;
+                    f.rows |= (row < sl->end[ti.e] ? 1u : 0u) << i;
+                    const float *p = g.a_scales + min64(row, g.rows - 1) + static_cast<int64_t>(kb0) * g.rows;
 #pragma unroll
-                        for (int j = 0; j < GROUP; ++j)
-                            if (kb0 + j < num_kb)
-                                w[i] |= code(__ldg(p + static_cast<int64_t>(j) * g.rows), row < row_end) << (8 * j);
-                    }
-                    // lanes 0-3 and 4-7: the two 128-column halves of W
-                    uint32_t e = 0;
-                    if (lane < 8) {
-                        const int j = lane & 3, h = lane >> 2;
-                        const int nb = EPI == EPI_SWIGLU ? ti.n_tile : min(ti.n_tile * 2 + h, nblocks - 1);
-                        const float *p = (EPI == EPI_SWIGLU && h ? g.w3_scales : g.w_scales) +
-                                         (static_cast<int64_t>(ti.e) * nblocks + nb) * num_kb;
-                        if (kb0 + j < num_kb) e = code(__ldg(p + kb0 + j), true) << (8 * j);
-                    }
-                    e |= __shfl_xor_sync(0xffffffffu, e, 1);
-                    e |= __shfl_xor_sync(0xffffffffu, e, 2);
-                    const uint32_t w0 = __shfl_sync(0xffffffffu, e, 0), w1 = __shfl_sync(0xffffffffu, e, 4);
-                    if (!__all_sync(0xffffffffu, mbar_wait(&ctl->sempty[mine], phase, abort_flag, g.status))) {
-                        ok = false;
-                        break;
-                    }
-                    phase ^= 1u;
-                    uint8_t *dst = ctl->scales[mine] + lane * 16;
-                    st16(dst, make_uint4(w[0], w[1], w[2], w[3]));
-                    st16(dst + 512, make_uint4(w0, w0, w0, w0));
-                    st16(dst + 1024, make_uint4(w1, w1, w1, w1));
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (PAIR) mbar_arrive_cluster(sfull);
-                        else mbar_arrive(&ctl->sfull[mine]);
-                    }
+                    for (int j = 0; j < GROUP; ++j)
+                        f.a[i][j] = kb0 + j < num_kb ? load_ahead(p + static_cast<int64_t>(j) * g.rows) : 1.0f;
                 }
+                const int j = kb0 + (lane & 3), h = lane >> 2 & 1;
+                const int nb = EPI == EPI_SWIGLU ? ti.n_tile : min(ti.n_tile * 2 + h, nblocks - 1);
+                const float *p = (EPI == EPI_SWIGLU && h ? g.w3_scales : g.w_scales) +
+                                 (static_cast<int64_t>(ti.e) * nblocks + nb) * num_kb;
+                f.w = j < num_kb ? load_ahead(p + j) : 1.0f;
+            };
+            // exponent codes; a scale that is no power of two (zero,
+            // negative, any mantissa) is reported
+            auto code = [&](float v, bool counts) {
+                const uint32_t b = __float_as_uint(v), e = b >> 23;
+                odd_scale |= counts && (e == 0 || e > 255 || (e < 255 && (b & 0x7FFFFFu) != 0));
+                return e & 255u;
+            };
+            auto next = [&](Fetch &f) {  // two groups on: the warps alternate
+                f.gi += 2;
+                while (f.gi >= groups) {
+                    f.gi -= groups;
+                    f.t += step;
+                }
+            };
+            Fetch now, then;
+            now.t = first;
+            now.gi = warp - 4;
+            next(now);
+            fetch(now);
+            for (uint32_t group = warp - 2; now.t < total; group += 2) {
+                then.t = now.t;
+                then.gi = now.gi;
+                next(then);
+                fetch(then);
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    w[i] = 0;
+#pragma unroll
+                    for (int j = 0; j < GROUP; ++j) w[i] |= code(now.a[i][j], now.rows >> i & 1u) << (8 * j);
+                }
+                uint32_t e = code(now.w, true) << (8 * (lane & 3));
+                e |= __shfl_xor_sync(0xffffffffu, e, 1);
+                e |= __shfl_xor_sync(0xffffffffu, e, 2);
+                const uint32_t w0 = __shfl_sync(0xffffffffu, e, 0), w1 = __shfl_sync(0xffffffffu, e, 4);
+                const uint32_t slot = group % SLOTS;
+                if (!__all_sync(0xffffffffu,
+                                mbar_wait(&ctl->sempty[slot], (group / SLOTS & 1u) ^ 1u, abort_flag, g.status)))
+                    break;
+                uint8_t *dst = ctl->scales[slot] + lane * 16;
+                st16(dst, make_uint4(w[0], w[1], w[2], w[3]));
+                st16(dst + 512, make_uint4(w0, w0, w0, w0));
+                st16(dst + 1024, make_uint4(w1, w1, w1, w1));
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (PAIR) mbar_arrive_cluster(mapa_shared(smem_u32(&ctl->sfull[slot]), 0));
+                    else mbar_arrive(&ctl->sfull[slot]);
+                }
+                now = then;
             }
             if (odd_scale) set_status(g.status, 1);
         }
@@ -452,7 +498,6 @@ __device__ __forceinline__ void
             } else if constexpr (EPI == EPI_GELU) {
                 const int c0 = n0 + half * 128;
                 if (c0 >= g.n_out) continue;
-                float h[128];
                 uint32_t m = 0;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -462,8 +507,9 @@ __device__ __forceinline__ void
                         bias8(bias, c0 + chunk(c, 4) * 32 + 8 * j, g.n_out, b);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            h[c * 32 + 8 * j + i] = gelu_erf(__uint_as_float(v[c][8 * j + i]) + b[i]);
-                            m = max(m, abs_bits(h[c * 32 + 8 * j + i]));
+                            const float h = gelu_erf(__uint_as_float(v[c][8 * j + i]) + b[i]);
+                            v[c][8 * j + i] = __float_as_uint(h);
+                            m = max(m, abs_bits(h));
                         }
                     }
                 }
@@ -471,7 +517,12 @@ __device__ __forceinline__ void
                 if (row < row_end) {
                     uint8_t *out = static_cast<uint8_t *>(g.out) + row * g.n_out;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) store_h32(h + 32 * c, s.y, out, c0 + chunk(c, 4) * 32, g.n_out);
+                    for (int c = 0; c < 4; ++c) {
+                        float h[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) h[i] = __uint_as_float(v[c][i]);
+                        store_h32(h, s.y, out, c0 + chunk(c, 4) * 32, g.n_out);
+                    }
                     g.h_scales[static_cast<int64_t>(min(ti.n_tile * 2 + half, nblocks - 1)) * g.rows + row] = s.x;
                 }
             } else {
