@@ -550,10 +550,10 @@ MOE_API size_t moe_balance_loss_workspace_size(int64_t N, int32_t E, int32_t S);
  * [1], counts_out [S, E] (cnt, int32) and seq_weight_out [S] (E / (S' T_s^2),
  * 0 without counted tokens), which the gradient below takes.  Sums over
  * tokens are fixed-order fp32 inside a chunk and fp64 above it: equal inputs
- * give equal bits.  dev_status (may be NULL): an id outside [0, E) of a
- * counted token is left out and sets MOE_ERR_BAD_EXPERT_ID; seq_offsets that
- * decrease or leave 0 .. N set MOE_ERR_INVALID_ARG (the outputs are then
- * meaningless).  E <= 256, k <= min(E, 16), N k < 2^31.
+ * give equal bits.  dev_status (may be NULL) is written by the call: MOE_OK;
+ * MOE_ERR_BAD_EXPERT_ID for an id outside [0, E) of a counted token, which is
+ * left out; MOE_ERR_INVALID_ARG for seq_offsets that decrease or leave 0 .. N
+ * (the other outputs are then meaningless).  E <= 256, k <= min(E, 16), N k < 2^31.
  */
 MOE_API moe_status moe_balance_loss(int32_t dtype, int32_t scores, const void *logits, const int32_t *topk_ids,
                                     const int32_t *seq_offsets, const uint8_t *token_mask, int64_t N, int32_t E,

@@ -412,45 +412,69 @@ def moe_backward(cfg: MoeConfig, x: torch.Tensor, W_g: torch.Tensor, W1: torch.T
 
 
 # ------------------------------------------- block-scaled e4m3, balance loss
+#
+# These calls are a few microseconds on the GPU at their smallest, so their
+# bindings keep the host's part short: pointers and streams go to ctypes as
+# plain integers, and a device or stream is made current only where it is not.
+
+_HERE = contextlib.nullcontext()
+_E4M3, _F32, _BF16, _I32 = torch.float8_e4m3fn, torch.float32, torch.bfloat16, torch.int32
+
 
 def _fp8_blocks(n: int) -> int:
     return -(-n // 128)
 
 
-def _on(t: torch.Tensor, stream):
+def _on(where: str, t: torch.Tensor, stream):
     """The device of t, and the given stream, current for a call's allocations and launches."""
-    if not t.is_cuda:
-        raise ValueError("tensor arguments must live on a CUDA device")
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError(f"{where}: tensor arguments must live on a CUDA device")
     if stream is not None:
-        if stream.device != t.device:
-            raise ValueError(f"stream of {stream.device} for tensors on {t.device}")
+        if stream.device != dev:
+            raise ValueError(f"{where}: stream of {stream.device} for tensors on {dev}")
         return torch.cuda.stream(stream)
-    if t.device.index != torch.cuda.current_device():
-        return torch.cuda.device(t.device)
-    return contextlib.nullcontext()
+    return _HERE if dev.index == torch._C._cuda_getDevice() else torch.cuda.device(dev)
 
 
-def _arg(where: str, name: str, t: torch.Tensor, dtype, shape, device) -> ctypes.c_void_p:
-    """Pointer of a tensor argument after checking its type, shape, device and layout."""
-    if t.dtype != dtype or t.shape != shape:
+def _raw_stream(dev: torch.device) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _arg(where: str, name: str, t: torch.Tensor, dtype, shape, device) -> int:
+    """Address of a tensor argument after checking its type, shape, device and layout."""
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{where}: {name} must be {dtype} of shape {list(shape)}, got {t.dtype} of {list(t.shape)}")
     if t.device != device:
         raise ValueError(f"{where}: {name} is on {t.device}, expected {device}")
     if not t.is_contiguous():
         raise ValueError(f"{where}: {name} must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
+
+
+def _workspace_arg(where: str, ws: torch.Tensor, device) -> Tuple[int, int]:
+    """(address, bytes) of a workspace tensor."""
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"{where}: ws must be contiguous and on {device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def _float_dtype(where: str, name: str, t: torch.Tensor) -> int:
-    if t.dtype == torch.bfloat16:
+    """The library's code of a float tensor's type; the tensor must be contiguous."""
+    if not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be contiguous")
+    if t.dtype is _BF16:
         return 1
-    if t.dtype == torch.float32:
+    if t.dtype is _F32:
         return 0
     raise ValueError(f"{where}: {name} must be float32 or bfloat16, got {t.dtype}")
 
 
 def _aligned_bytes(n: int, device) -> torch.Tensor:
     """n device bytes on a 256-byte boundary."""
+    raw = torch.empty(n, dtype=torch.uint8, device=device)
+    if raw.data_ptr() % 256 == 0:
+        return raw
     raw = torch.empty(n + 256, dtype=torch.uint8, device=device)
     off = (-raw.data_ptr()) % 256
     return raw[off:off + n]
@@ -464,10 +488,11 @@ def moe_quantize_rows(x: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch
         raise ValueError(f"{where}: x must be [rows, cols]")
     dtype, dev = _float_dtype(where, "x", x), x.device
     rows, cols = x.shape
-    with _on(x, stream):
-        q = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=dev)
-        scales = torch.empty((_fp8_blocks(cols), rows), dtype=torch.float32, device=dev)
-        rc = library().moe_quantize_rows(dtype, _ptr(x), rows, cols, _ptr(q), _ptr(scales), _stream())
+    with _on(where, x, stream):
+        q = torch.empty((rows, cols), dtype=_E4M3, device=dev)
+        scales = torch.empty((_fp8_blocks(cols), rows), dtype=_F32, device=dev)
+        rc = library().moe_quantize_rows(dtype, x.data_ptr(), rows, cols, q.data_ptr(), scales.data_ptr(),
+                                         _raw_stream(dev))
     _check(rc, where)
     return q, scales
 
@@ -481,11 +506,11 @@ def moe_quantize_weights(W: torch.Tensor, transpose: bool = False, stream=None) 
     dtype, dev = _float_dtype(where, "W", W), W.device
     E, rows, cols = W.shape
     r, c = (cols, rows) if transpose else (rows, cols)
-    with _on(W, stream):
-        q = torch.empty((E, r, c), dtype=torch.float8_e4m3fn, device=dev)
-        scales = torch.empty((E, _fp8_blocks(r), _fp8_blocks(c)), dtype=torch.float32, device=dev)
-        rc = library().moe_quantize_weights(dtype, _ptr(W), E, rows, cols, int(bool(transpose)), _ptr(q),
-                                            _ptr(scales), _stream())
+    with _on(where, W, stream):
+        q = torch.empty((E, r, c), dtype=_E4M3, device=dev)
+        scales = torch.empty((E, _fp8_blocks(r), _fp8_blocks(c)), dtype=_F32, device=dev)
+        rc = library().moe_quantize_weights(dtype, W.data_ptr(), E, rows, cols, int(bool(transpose)), q.data_ptr(),
+                                            scales.data_ptr(), _raw_stream(dev))
     _check(rc, where)
     return q, scales
 
@@ -503,27 +528,27 @@ def moe_expert_matmul_fp8(a: Tuple[torch.Tensor, torch.Tensor], offsets: torch.T
     (aq, asc), (wq, wsc) = a, w
     if aq.dim() != 2 or wq.dim() != 3:
         raise ValueError(f"{where}: a must be [rows, k] and w [E, n, k]")
-    (rows, k), (E, n, _), dev, e4m3, f32 = aq.shape, wq.shape, aq.device, torch.float8_e4m3fn, torch.float32
+    (rows, k), (E, n, _), dev = aq.shape, wq.shape, aq.device
     kb = _fp8_blocks(k)
-    if out_dtype not in (torch.bfloat16, f32):
+    if out_dtype is not _BF16 and out_dtype is not _F32:
         raise ValueError(f"{where}: out_dtype must be bfloat16 or float32, got {out_dtype}")
-    with _on(aq, stream):
-        out = out if out is not None else torch.empty((rows, n), dtype=out_dtype, device=dev)
+    with _on(where, aq, stream):
+        if out is None:
+            out = torch.empty((rows, n), dtype=out_dtype, device=dev)
         rc = library().moe_expert_matmul_fp8(
-            rows, n, k, E, _arg(where, "a", aq, e4m3, (rows, k), dev),
-            _arg(where, "a's scales", asc, f32, (kb, rows), dev),
-            _arg(where, "offsets", offsets, torch.int32, (E + 1,), dev), _arg(where, "w", wq, e4m3, (E, n, k), dev),
-            _arg(where, "w's scales", wsc, f32, (E, _fp8_blocks(n), kb), dev), int(bool(any_scales)),
-            int(out_dtype == torch.bfloat16),
-            _arg(where, "out", out, out_dtype, (rows, n), dev),
-            _arg(where, "status", status, torch.int32, (1,), dev) if status is not None else None, _stream())
+            rows, n, k, E, _arg(where, "a", aq, _E4M3, (rows, k), dev),
+            _arg(where, "a's scales", asc, _F32, (kb, rows), dev),
+            _arg(where, "offsets", offsets, _I32, (E + 1,), dev), _arg(where, "w", wq, _E4M3, (E, n, k), dev),
+            _arg(where, "w's scales", wsc, _F32, (E, _fp8_blocks(n), kb), dev), int(bool(any_scales)),
+            int(out_dtype is _BF16), _arg(where, "out", out, out_dtype, (rows, n), dev),
+            None if status is None else _arg(where, "status", status, _I32, (1,), dev), _raw_stream(dev))
     _check(rc, where)
     return out
 
 
 def moe_expert_ffn_fp8_workspace(cfg: MoeConfig, device=None) -> torch.Tensor:
     """A device workspace for moe_expert_ffn_fp8 (256-byte aligned)."""
-    n = int(library().moe_expert_ffn_fp8_workspace_size(ctypes.byref(cfg)))
+    n = library().moe_expert_ffn_fp8_workspace_size(ctypes.byref(cfg))
     if n == 0:
         raise MoeError(2, "moe_expert_ffn_fp8_workspace_size")
     return _aligned_bytes(n, device or "cuda")
@@ -539,46 +564,44 @@ def moe_expert_ffn_fp8(cfg: MoeConfig, x_sorted: torch.Tensor, offsets: torch.Te
     and the result bf16.  any_scales as for moe_expert_matmul_fp8.  Rows outside every slice keep what ``out``
     held."""
     where, dev = "moe_expert_ffn_fp8", x_sorted.device
-    e4m3, f32, bf16 = torch.float8_e4m3fn, torch.float32, torch.bfloat16
     E, d, F, A = cfg.E, cfg.d_model, cfg.d_ff, cfg.N * cfg.k
-
-    def pair(name, w, rows, cols):
-        if w is None:
-            return None, None
-        return (_arg(where, name, w[0], e4m3, (E, rows, cols), dev).value,
-                _arg(where, name + "'s scales", w[1], f32, (E, _fp8_blocks(rows), _fp8_blocks(cols)), dev).value)
-
-    def one(name, t, dtype, shape):
-        return None if t is None else _arg(where, name, t, dtype, shape, dev).value
-
-    with _on(x_sorted, stream):
-        ws = ws if ws is not None else moe_expert_ffn_fp8_workspace(cfg, dev)
-        out = out if out is not None else torch.empty((A, d), dtype=bf16, device=dev)
-        w = Fp8Experts(*pair("W1", W1, F, d), *pair("W3", W3, F, d), *pair("W2", W2, d, F),
-                       one("b1", b1, bf16, (E, F)), one("b2", b2, bf16, (E, d)), int(bool(any_scales)))
+    db, Fb = _fp8_blocks(d), _fp8_blocks(F)
+    with _on(where, x_sorted, stream):
+        if ws is None:
+            ws = moe_expert_ffn_fp8_workspace(cfg, dev)
+        if out is None:
+            out = torch.empty((A, d), dtype=_BF16, device=dev)
+        w = Fp8Experts(
+            _arg(where, "W1", W1[0], _E4M3, (E, F, d), dev), _arg(where, "W1's scales", W1[1], _F32, (E, Fb, db), dev),
+            None if W3 is None else _arg(where, "W3", W3[0], _E4M3, (E, F, d), dev),
+            None if W3 is None else _arg(where, "W3's scales", W3[1], _F32, (E, Fb, db), dev),
+            _arg(where, "W2", W2[0], _E4M3, (E, d, F), dev), _arg(where, "W2's scales", W2[1], _F32, (E, db, Fb), dev),
+            None if b1 is None else _arg(where, "b1", b1, _BF16, (E, F), dev),
+            None if b2 is None else _arg(where, "b2", b2, _BF16, (E, d), dev), int(bool(any_scales)))
         rc = library().moe_expert_ffn_fp8(
-            ctypes.byref(cfg), _arg(where, "x_sorted", x_sorted, bf16, (A, d), dev),
-            _arg(where, "offsets", offsets, torch.int32, (E + 1,), dev), ctypes.byref(w),
-            _arg(where, "out", out, bf16, (A, d), dev), one("status", status, torch.int32, (1,)), _ptr(ws),
-            ws.numel(), _stream())
+            ctypes.byref(cfg), _arg(where, "x_sorted", x_sorted, _BF16, (A, d), dev),
+            _arg(where, "offsets", offsets, _I32, (E + 1,), dev), ctypes.byref(w),
+            _arg(where, "out", out, _BF16, (A, d), dev),
+            None if status is None else _arg(where, "status", status, _I32, (1,), dev),
+            *_workspace_arg(where, ws, dev), _raw_stream(dev))
     _check(rc, where)
     return out
 
 
 def _sequences(where: str, logits: torch.Tensor, seq_offsets, token_mask):
-    """(N, E, S, seq_offsets pointer, mask pointer) of the balance loss."""
+    """(N, E, S, seq_offsets address, mask address) of the balance loss."""
     if logits.dim() != 2:
         raise ValueError(f"{where}: logits must be [N, E]")
     N, E = logits.shape
-    if seq_offsets is not None and (seq_offsets.dim() != 1 or seq_offsets.numel() < 2):
-        raise ValueError(f"{where}: seq_offsets must be [S + 1] with S >= 1")
-    S = seq_offsets.numel() - 1 if seq_offsets is not None else 1
-    off = (_arg(where, "seq_offsets", seq_offsets, torch.int32, (S + 1,), logits.device)
-           if seq_offsets is not None else None)
-    mask = None
+    S, off, mask = 1, None, None
+    if seq_offsets is not None:
+        S = seq_offsets.numel() - 1
+        if S < 1:
+            raise ValueError(f"{where}: seq_offsets must be [S + 1] with S >= 1")
+        off = _arg(where, "seq_offsets", seq_offsets, _I32, (S + 1,), logits.device)
     if token_mask is not None:
-        mask = _arg(where, "token_mask", token_mask, torch.uint8 if token_mask.dtype == torch.uint8 else torch.bool,
-                    (N,), logits.device)
+        kind = torch.uint8 if token_mask.dtype is torch.uint8 else torch.bool
+        mask = _arg(where, "token_mask", token_mask, kind, (N,), logits.device)
     return N, E, S, off, mask
 
 
@@ -591,25 +614,25 @@ def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, seq_offsets: 
     "softmax" or "sigmoid" (normalised).  Returns loss [1], counts [S, E] int32, seq_weight [S] (for the gradient)
     and status [1] int32 (6: an expert id out of range, 1: bad seq_offsets)."""
     where, dev = "moe_balance_loss", logits.device
-    dtype = _float_dtype(where, "logits", logits)
     N, E, S, off, mask = _sequences(where, logits, seq_offsets, token_mask)
+    dtype = _float_dtype(where, "logits", logits)
     if topk_ids.dim() != 2:
         raise ValueError(f"{where}: topk_ids must be [N, k]")
-    k = topk_ids.shape[1]
-    with _on(logits, stream):
+    k, lib = topk_ids.shape[1], library()
+    with _on(where, logits, stream):
         if ws is None:
-            n = int(library().moe_balance_loss_workspace_size(N, E, S))
+            n = lib.moe_balance_loss_workspace_size(N, E, S)
             if n == 0:
                 raise MoeError(2, "moe_balance_loss_workspace_size")
             ws = _aligned_bytes(n, dev)
-        loss = torch.empty(1, dtype=torch.float32, device=dev)
-        counts = torch.empty((S, E), dtype=torch.int32, device=dev)
-        weight = torch.empty(S, dtype=torch.float32, device=dev)
-        status = torch.zeros(1, dtype=torch.int32, device=dev)
-        rc = library().moe_balance_loss(dtype, SCORES[scores], _ptr(logits),
-                                        _arg(where, "topk_ids", topk_ids, torch.int32, (N, k), dev), off, mask, N, E,
-                                        k, S, _ptr(loss), _ptr(counts), _ptr(weight), _ptr(status), _ptr(ws),
-                                        ws.numel(), _stream())
+        loss = torch.empty(1, dtype=_F32, device=dev)
+        counts = torch.empty((S, E), dtype=_I32, device=dev)
+        weight = torch.empty(S, dtype=_F32, device=dev)
+        status = torch.empty(1, dtype=_I32, device=dev)
+        rc = lib.moe_balance_loss(dtype, SCORES[scores], logits.data_ptr(),
+                                  _arg(where, "topk_ids", topk_ids, _I32, (N, k), dev), off, mask, N, E, k, S,
+                                  loss.data_ptr(), counts.data_ptr(), weight.data_ptr(), status.data_ptr(),
+                                  *_workspace_arg(where, ws, dev), _raw_stream(dev))
     _check(rc, where)
     return {"loss": loss, "counts": counts, "seq_weight": weight, "status": status}
 
@@ -621,16 +644,16 @@ def moe_balance_loss_backward(logits: torch.Tensor, fwd: Dict[str, torch.Tensor]
     """dlogits [N, E] f32 of coef * dloss * loss, for the same arguments as moe_balance_loss and its result ``fwd``
     (dloss: an upstream gradient [1] f32 on the device)."""
     where, dev = "moe_balance_loss_backward", logits.device
-    dtype = _float_dtype(where, "logits", logits)
     N, E, S, off, mask = _sequences(where, logits, seq_offsets, token_mask)
-    with _on(logits, stream):
-        dlogits = torch.empty((N, E), dtype=torch.float32, device=dev)
+    dtype = _float_dtype(where, "logits", logits)
+    with _on(where, logits, stream):
+        dlogits = torch.empty((N, E), dtype=_F32, device=dev)
         rc = library().moe_balance_loss_backward(
-            dtype, SCORES[scores], _ptr(logits), off, mask, N, E, S,
-            _arg(where, "counts", fwd["counts"], torch.int32, (S, E), dev),
-            _arg(where, "seq_weight", fwd["seq_weight"], torch.float32, (S,), dev), float(coef),
-            _arg(where, "dloss", dloss, torch.float32, (1,), dev) if dloss is not None else None, _ptr(dlogits),
-            _stream())
+            dtype, SCORES[scores], logits.data_ptr(), off, mask, N, E, S,
+            _arg(where, "counts", fwd["counts"], _I32, (S, E), dev),
+            _arg(where, "seq_weight", fwd["seq_weight"], _F32, (S,), dev), coef,
+            None if dloss is None else _arg(where, "dloss", dloss, _F32, (1,), dev), dlogits.data_ptr(),
+            _raw_stream(dev))
     _check(rc, where)
     return dlogits
 

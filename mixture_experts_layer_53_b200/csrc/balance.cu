@@ -32,6 +32,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 4;       // tokens a lane group loads at once
 constexpr int kMinChunk = 32;
 constexpr int kMaxChunks = 1184;  // 148 SMs x 8 CTAs
+constexpr int kBadId = 1, kBadCut = 2;  // flags of a segment or sequence
 
 __host__ __device__ __forceinline__ int64_t align256(int64_t b) { return (b + 255) & ~static_cast<int64_t>(255); }
 
@@ -59,8 +60,8 @@ Plan make_plan(int64_t N, int E, int S)
     p.ticket = take(4);
     p.psum = take(p.slots * E * 4);
     p.cnt = take(p.slots * E * 4);
-    p.tok = take(p.slots * 4);
-    p.tokens = take(static_cast<int64_t>(S) * 4);
+    p.tok = take(p.slots * 8);                        // int2: valid tokens, flags
+    p.tokens = take(static_cast<int64_t>(S) * 8);     // int2
     p.dot = take(static_cast<int64_t>(S) * p.groups * 8);
     p.total = o;
     return p;
@@ -88,20 +89,26 @@ struct Seqs {
     }
 };
 
-// Four consecutive logits from expert e on; -inf past E.
-__device__ __forceinline__ float4 load4(const float *p, int e, int E, bool vec)
+// Four consecutive logits from expert e on; -inf past E.  The first pass
+// leaves them in L2 for the second (the gradient's), which reads them last.
+template <bool LAST, typename V> __device__ __forceinline__ V load_vec(const V *p)
+{
+    return LAST ? __ldcs(p) : __ldg(p);
+}
+template <bool LAST> __device__ __forceinline__ float4 load4(const float *p, int e, int E, bool vec)
 {
     const float ninf = -INFINITY;
-    if (vec) return e < E ? __ldcs(reinterpret_cast<const float4 *>(p + e)) : make_float4(ninf, ninf, ninf, ninf);
+    if (vec) return e < E ? load_vec<LAST>(reinterpret_cast<const float4 *>(p + e)) : make_float4(ninf, ninf, ninf, ninf);
     return make_float4(e < E ? p[e] : ninf, e + 1 < E ? p[e + 1] : ninf, e + 2 < E ? p[e + 2] : ninf,
                        e + 3 < E ? p[e + 3] : ninf);
 }
+template <bool LAST>
 __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p, int e, int E, bool vec)
 {
     const float ninf = -INFINITY;
     if (vec) {
         if (e >= E) return make_float4(ninf, ninf, ninf, ninf);
-        const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p + e));
+        const uint2 v = load_vec<LAST>(reinterpret_cast<const uint2 *>(p + e));
         return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
                            __uint_as_float(v.y & 0xFFFF0000u));
     }
@@ -124,42 +131,66 @@ template <int G> __device__ __forceinline__ float group_max(float v)
 
 constexpr float kLog2e = 1.44269504f;
 
-// Normalised scores of one token, in place of its logits z; with `slope` also
-// m = 1 - sigmoid(z).  Every lane of the warp takes part.  A token whose
+// Normalised scores of one token, in place of its logits z; with m also
+// m = 1 - sigmoid(z).  Every lane of the warp takes part; a token that is not
+// used has logits of -inf throughout.  A token whose
 // logits are all -inf has no scores: p = 0.  The exponent is the rounded
-// product of z - max (or |z|) and log2 e, so its error is relative to it:
-// about 1e-7 for the scores that matter, 6e-8 |z - max| for small ones.
+// product of z - max (or z) and log2 e, so its error is relative to it: about
+// 1e-7 for the scores that matter, 6e-8 |z - max| for small ones.
 template <int G, int NV, bool SIGMOID>
-__device__ __forceinline__ void scores(float (&z)[4 * NV], float *m)
+__device__ __forceinline__ void scores(float (&z)[4 * NV], float *m, bool use)
 {
-    float top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < 4 * NV; ++i) top = fmaxf(top, z[i]);
-    top = group_max<G>(top);
     float sum = 0.0f;
     if constexpr (!SIGMOID) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 4 * NV; ++i) top = fmaxf(top, z[i]);
+        top = group_max<G>(top);
         const float shift = top == -INFINITY ? 0.0f : top;
 #pragma unroll
         for (int i = 0; i < 4 * NV; ++i) {
             z[i] = ex2_approx((z[i] - shift) * kLog2e);
             sum += z[i];
         }
+        sum = group_sum<G>(sum);
     } else {
-        // sigma(z) = a / (1 + a') with exponentials of non-positive arguments
-        // only.  If every logit is far below zero the sigmoids underflow but
-        // their ratios do not: e^-top then multiplies all of them.
-        const float low = (top < -20.0f && top != -INFINITY) ? top : 0.0f;
+        // sigma(z) = 1 / (1 + e), m = e sigma(z) with e = e^-z, held below
+        // 2^127: the reciprocal is then 0 (a sigmoid under 2^-126), and
+        // e times it no NaN.
+        float p[4 * NV];
 #pragma unroll
         for (int i = 0; i < 4 * NV; ++i) {
-            const float e = ex2_approx(fabsf(z[i]) * -kLog2e);
-            const float r = rcp_approx(1.0f + e);
-            const bool pos = z[i] >= 0.0f;
-            if (m) m[i] = (pos ? e : 1.0f) * r;
-            z[i] = low != 0.0f ? ex2_approx((z[i] - low) * kLog2e) * r : (pos ? 1.0f : e) * r;
-            sum += z[i];
+            const float e = ex2_approx(fminf(z[i] * -kLog2e, 127.0f));
+            p[i] = z[i] == z[i] ? rcp_approx(1.0f + e) : z[i];
+            if (m) m[i] = e * p[i];
+            sum += p[i];
         }
+        sum = group_sum<G>(sum);
+        if (__any_sync(0xffffffffu, use && sum < 1e-6f)) {
+            // Every logit of a token is far below zero: the sigmoids underflow
+            // but their ratios, those of e^z, do not.
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 4 * NV; ++i) top = fmaxf(top, z[i]);
+            top = group_max<G>(top);
+            const bool low = use && sum < 1e-6f;
+            const float shift = top == -INFINITY ? 0.0f : top;
+            float ratios = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4 * NV; ++i) {
+                const float r = ex2_approx((z[i] - shift) * kLog2e);
+                ratios += r;
+                if (low) {
+                    p[i] = r;
+                    if (m) m[i] = 1.0f;
+                }
+            }
+            ratios = group_sum<G>(ratios);
+            if (low) sum = ratios;
+        }
+#pragma unroll
+        for (int i = 0; i < 4 * NV; ++i) z[i] = p[i];
     }
-    sum = group_sum<G>(sum);
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
     for (int i = 0; i < 4 * NV; ++i) z[i] *= inv;
@@ -171,7 +202,7 @@ __global__ void __launch_bounds__(kThreads) balance_partial_kernel(const Balance
     pdl_enter();
     __shared__ float red[kWarps][G * 4 * NV];
     __shared__ int cnt[kMaxE];
-    __shared__ int valid;
+    __shared__ int valid, bad;
     constexpr int GROUPS = kThreads / G;
     uint8_t *ws = static_cast<uint8_t *>(a.ws);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -187,7 +218,7 @@ __global__ void __launch_bounds__(kThreads) balance_partial_kernel(const Balance
         if (lo >= hi) continue;
         __syncthreads();  // the last segment's shared sums have been read
         for (int i = threadIdx.x; i < a.E; i += kThreads) cnt[i] = 0;
-        if (threadIdx.x == 0) valid = 0;
+        if (threadIdx.x == 0) valid = bad = 0;
         __syncthreads();
         float sum[4 * NV];
 #pragma unroll
@@ -202,7 +233,7 @@ __global__ void __launch_bounds__(kThreads) balance_partial_kernel(const Balance
                 use[u] = n < hi && (!a.mask || a.mask[n] != 0);
 #pragma unroll
                 for (int j = 0; j < NV; ++j)
-                    v[u][j] = use[u] ? load4(logits + n * a.E, (j * G + q) * 4, a.E, vec)
+                    v[u][j] = use[u] ? load4<false>(logits + n * a.E, (j * G + q) * 4, a.E, vec)
                                      : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
             }
 #pragma unroll
@@ -215,7 +246,7 @@ __global__ void __launch_bounds__(kThreads) balance_partial_kernel(const Balance
                     z[4 * j + 2] = v[u][j].z;
                     z[4 * j + 3] = v[u][j].w;
                 }
-                scores<G, NV, SIGMOID>(z, nullptr);  // an unused token: all -inf, p = 0
+                scores<G, NV, SIGMOID>(z, nullptr, use[u]);
                 mine += use[u] && q == 0;
 #pragma unroll
                 for (int i = 0; i < 4 * NV; ++i) sum[i] += z[i];
@@ -226,7 +257,7 @@ __global__ void __launch_bounds__(kThreads) balance_partial_kernel(const Balance
             if (a.mask && a.mask[lo + i / a.k] == 0) continue;
             const int e = a.ids[lo * a.k + i];
             if (static_cast<unsigned>(e) < static_cast<unsigned>(a.E)) atomicAdd(&cnt[e], 1);
-            else set_status(a.status, kDevBadExpertId);
+            else bad = kBadId;
         }
         if (mine) atomicAdd(&valid, mine);
         // over the warp's lane groups, then over the warps
@@ -248,7 +279,7 @@ __global__ void __launch_bounds__(kThreads) balance_partial_kernel(const Balance
             reinterpret_cast<float *>(ws + p.psum)[slot * a.E + e] = t;
             reinterpret_cast<int *>(ws + p.cnt)[slot * a.E + e] = cnt[e];
         }
-        if (threadIdx.x == 0) reinterpret_cast<int *>(ws + p.tok)[slot] = valid;
+        if (threadIdx.x == 0) reinterpret_cast<int2 *>(ws + p.tok)[slot] = make_int2(valid, bad);
     }
 }
 
@@ -263,8 +294,9 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(const BalanceArgs 
     __shared__ bool last;
     uint8_t *ws = static_cast<uint8_t *>(a.ws);
     const float *psum = reinterpret_cast<const float *>(ws + p.psum);
-    const int *cnt = reinterpret_cast<const int *>(ws + p.cnt), *tok = reinterpret_cast<const int *>(ws + p.tok);
-    int *tokens = reinterpret_cast<int *>(ws + p.tokens);
+    const int *cnt = reinterpret_cast<const int *>(ws + p.cnt);
+    const int2 *tok = reinterpret_cast<const int2 *>(ws + p.tok);
+    int2 *tokens = reinterpret_cast<int2 *>(ws + p.tokens);
     double *dot = reinterpret_cast<double *>(ws + p.dot);
     uint32_t *ticket = reinterpret_cast<uint32_t *>(ws + p.ticket);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -274,7 +306,7 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(const BalanceArgs 
     const int64_t lo = seqs.at(s), hi = seqs.at(s + 1);
     const int64_t c0 = lo / p.chunk, c1 = hi > lo ? (hi - 1) / p.chunk + 1 : c0;
     double P = 0.0;
-    int n = 0, T = 0;
+    int n = 0, T = 0, odd = 0;
     if (e < a.E) {
 #pragma unroll 4
         for (int64_t c = c0 + warp; c < c1; c += warps) {
@@ -283,7 +315,11 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(const BalanceArgs 
         }
     }
     if (gr == 0)
-        for (int64_t c = c0 + threadIdx.x; c < c1; c += blockDim.x) T += tok[c + s];
+        for (int64_t c = c0 + threadIdx.x; c < c1; c += blockDim.x) {
+            const int2 t = tok[c + s];
+            T += t.x;
+            odd |= t.y;
+        }
     dsum[warp][lane] = P;
     isum[warp][lane] = n;
     __syncthreads();
@@ -300,16 +336,23 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(const BalanceArgs 
     }
     __syncthreads();
     T = __reduce_add_sync(0xffffffffu, T);
-    if (lane == 0) isum[warp][0] = T;
+    odd = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(odd));
+    if (lane == 0) {
+        isum[warp][0] = T;
+        isum[warp][1] = odd;
+    }
     __syncthreads();
     if (threadIdx.x == 0) {
         if (gr == 0) {
-            int all = 0;
-            for (int w = 0; w < warps; ++w) all += isum[w][0];
-            tokens[s] = all;
+            int2 all = make_int2(0, 0);
+            for (int w = 0; w < warps; ++w) {
+                all.x += isum[w][0];
+                all.y |= isum[w][1];
+            }
             // offsets that decrease or leave 0 .. N
             if (a.seq_offsets && (a.seq_offsets[s] < 0 || a.seq_offsets[s + 1] < a.seq_offsets[s] || a.seq_offsets[s + 1] > a.N))
-                set_status(a.status, 1);
+                all.y |= kBadCut;
+            tokens[s] = all;
         }
         __threadfence();
         last = atomicAdd(ticket, 1u) + 1u == gridDim.x;
@@ -319,15 +362,27 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(const BalanceArgs 
     __threadfence();
     // sequences with tokens
     int full = 0;
-    for (int i = threadIdx.x; i < a.S; i += blockDim.x) full += __ldcg(tokens + i) > 0;
+    odd = 0;
+    for (int i = threadIdx.x; i < a.S; i += blockDim.x) {
+        const int2 t = __ldcg(tokens + i);
+        full += t.x > 0;
+        odd |= t.y;
+    }
     full = __reduce_add_sync(0xffffffffu, full);
-    if (lane == 0) isum[warp][0] = full;
+    odd = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(odd));
+    if (lane == 0) {
+        isum[warp][0] = full;
+        isum[warp][1] = odd;
+    }
     __syncthreads();
-    full = 0;
-    for (int w = 0; w < warps; ++w) full += isum[w][0];
+    full = odd = 0;
+    for (int w = 0; w < warps; ++w) {
+        full += isum[w][0];
+        odd |= isum[w][1];
+    }
     double L = 0.0;
     for (int i = threadIdx.x; i < a.S; i += blockDim.x) {
-        const double t = __ldcg(tokens + i);
+        const double t = __ldcg(tokens + i).x;
         double d = 0.0;
         for (int j = 0; j < p.groups; ++j) d += __ldcg(dot + static_cast<int64_t>(i) * p.groups + j);
         const double w = t > 0.0 ? a.E / (t * t * full) : 0.0;
@@ -343,6 +398,7 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(const BalanceArgs 
         L = 0.0;
         for (int w = 0; w < warps; ++w) L += dsum[w][0];
         *a.loss = static_cast<float>(L);
+        if (a.status) *a.status = odd & kBadCut ? kDevBadArgument : odd & kBadId ? kDevBadExpertId : kDevOk;
     }
 }
 
@@ -371,7 +427,7 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(const Balanc
             use[u] = n < end && (!a.mask || a.mask[n] != 0);
 #pragma unroll
             for (int j = 0; j < NV; ++j)
-                v[u][j] = use[u] ? load4(logits + n * a.E, (j * G + q) * 4, a.E, vec)
+                v[u][j] = use[u] ? load4<true>(logits + n * a.E, (j * G + q) * 4, a.E, vec)
                                  : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
         }
 #pragma unroll
@@ -403,7 +459,7 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(const Balanc
                 z[4 * j + 2] = v[u][j].z;
                 z[4 * j + 3] = v[u][j].w;
             }
-            scores<G, NV, SIGMOID>(z, SIGMOID ? m : nullptr);
+            scores<G, NV, SIGMOID>(z, SIGMOID ? m : nullptr, use[u]);
             float dot = 0.0f;
 #pragma unroll
             for (int i = 0; i < 4 * NV; ++i) dot = fmaf(z[i], c[i], dot);

@@ -410,7 +410,7 @@ __device__ __forceinline__ void
                 }
                 now = then;
             }
-            if (odd_scale) set_status(g.status, 1);
+            if (odd_scale) set_status(g.status, kDevBadArgument);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SUM_REGS));
