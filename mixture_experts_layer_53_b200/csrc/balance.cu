@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 4;       // tokens a lane group loads at once
+constexpr int kForwardUnroll = 4, kBackwardUnroll = 2;  // tokens a lane group handles at once
 constexpr int kMinChunk = 32;
 constexpr int kMaxChunks = 1184;  // 148 SMs x 8 CTAs
 constexpr int kBadId = 1, kBadCut = 2;  // flags of a segment or sequence
@@ -116,88 +116,148 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p, int e, int E, bo
                        e + 2 < E ? to_f32(p[e + 2]) : ninf, e + 3 < E ? to_f32(p[e + 3]) : ninf);
 }
 
-template <int G> __device__ __forceinline__ float group_sum(float v)
+// U values summed (or their maxima taken) over the G lanes of a group, the
+// independent shuffles of the U next to each other.
+template <int G, int U> __device__ __forceinline__ void group_sum(float (&v)[U])
 {
 #pragma unroll
-    for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+    for (int o = G / 2; o > 0; o >>= 1) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] += __shfl_xor_sync(0xffffffffu, v[u], o);
+    }
 }
-template <int G> __device__ __forceinline__ float group_max(float v)
+template <int G, int U> __device__ __forceinline__ void group_max(float (&v)[U])
 {
 #pragma unroll
-    for (int o = G / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
+    for (int o = G / 2; o > 0; o >>= 1) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = fmaxf(v[u], __shfl_xor_sync(0xffffffffu, v[u], o));
+    }
 }
 
 constexpr float kLog2e = 1.44269504f;
 
-// Normalised scores of one token, in place of its logits z; with m also
-// m = 1 - sigmoid(z).  Every lane of the warp takes part; a token that is not
-// used has logits of -inf throughout.  A token whose
-// logits are all -inf has no scores: p = 0.  The exponent is the rounded
-// product of z - max (or z) and log2 e, so its error is relative to it: about
-// 1e-7 for the scores that matter, 6e-8 |z - max| for small ones.
-template <int G, int NV, bool SIGMOID>
-__device__ __forceinline__ void scores(float (&z)[4 * NV], float *m, bool use)
+// min that keeps a NaN
+__device__ __forceinline__ float min_nan(float a, float b)
 {
-    float sum = 0.0f;
-    if constexpr (!SIGMOID) {
-        float top = -INFINITY;
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// The logits of U tokens (those at n0 + u * stride + group that are `use`d),
+// this lane's 4 NV experts of each; -inf where there is none.
+template <bool LAST, int G, int NV, int U, typename T>
+__device__ __forceinline__ void load_tokens(float (&z)[U][4 * NV], const T *logits, int64_t n, int64_t stride,
+                                            const bool (&use)[U], int q, int E, bool vec)
+{
 #pragma unroll
-        for (int i = 0; i < 4 * NV; ++i) top = fmaxf(top, z[i]);
-        top = group_max<G>(top);
-        const float shift = top == -INFINITY ? 0.0f : top;
+    for (int u = 0; u < U; ++u) {
 #pragma unroll
-        for (int i = 0; i < 4 * NV; ++i) {
-            z[i] = ex2_approx((z[i] - shift) * kLog2e);
-            sum += z[i];
+        for (int j = 0; j < NV; ++j) {
+            float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            if (use[u]) v = load4<LAST>(logits + (n + u * stride) * E, (j * G + q) * 4, E, vec);
+            z[u][4 * j] = v.x;
+            z[u][4 * j + 1] = v.y;
+            z[u][4 * j + 2] = v.z;
+            z[u][4 * j + 3] = v.w;
         }
-        sum = group_sum<G>(sum);
+    }
+}
+
+// Normalised scores of U tokens in place of their logits z; with SLOPE also m
+// = 1 - sigmoid(z).  Every lane of the warp takes part.  A token whose logits
+// are all -inf (or that is not used) has p = 0.  The exponent is the rounded
+// product of z - max (or z) and log2 e, so its error is relative to it: about
+// 1e-7 for the scores that matter, 6e-8 |z - max| for small ones.  `again`
+// loads the logits once more, for the rare path that needs them.
+template <int G, int NV, bool SIGMOID, bool SLOPE, int U, typename Again>
+__device__ __forceinline__ void scores(float (&z)[U][4 * NV], float (&m)[SLOPE ? U : 1][4 * NV], const bool (&use)[U],
+                                       Again &&again)
+{
+    constexpr int N = 4 * NV;
+    float sum[U], top[U];
+    auto tops = [&](const float (&x)[U][N]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            top[u] = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < N; ++i) top[u] = fmaxf(top[u], x[u][i]);
+        }
+        group_max<G>(top);
+#pragma unroll
+        for (int u = 0; u < U; ++u) top[u] = top[u] == -INFINITY ? 0.0f : top[u];
+    };
+    if constexpr (!SIGMOID) {
+        tops(z);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            sum[u] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                z[u][i] = ex2_approx((z[u][i] - top[u]) * kLog2e);
+                sum[u] += z[u][i];
+            }
+        }
+        group_sum<G>(sum);
     } else {
         // sigma(z) = 1 / (1 + e), m = e sigma(z) with e = e^-z, held below
         // 2^127: the reciprocal is then 0 (a sigmoid under 2^-126), and
         // e times it no NaN.
-        float p[4 * NV];
 #pragma unroll
-        for (int i = 0; i < 4 * NV; ++i) {
-            const float e = ex2_approx(fminf(z[i] * -kLog2e, 127.0f));
-            p[i] = z[i] == z[i] ? rcp_approx(1.0f + e) : z[i];
-            if (m) m[i] = e * p[i];
-            sum += p[i];
+        for (int u = 0; u < U; ++u) {
+            sum[u] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float e = ex2_approx(min_nan(z[u][i] * -kLog2e, 127.0f));
+                z[u][i] = rcp_approx(1.0f + e);
+                if constexpr (SLOPE) m[u][i] = e * z[u][i];
+                sum[u] += z[u][i];
+            }
         }
-        sum = group_sum<G>(sum);
-        if (__any_sync(0xffffffffu, use && sum < 1e-6f)) {
+        group_sum<G>(sum);
+        bool low = false;
+#pragma unroll
+        for (int u = 0; u < U; ++u) low |= use[u] && sum[u] < 1e-6f;
+        if (__any_sync(0xffffffffu, low)) {
             // Every logit of a token is far below zero: the sigmoids underflow
             // but their ratios, those of e^z, do not.
-            float top = -INFINITY;
+            float x[U][N], ratios[U];
+            again(x);
+            tops(x);
 #pragma unroll
-            for (int i = 0; i < 4 * NV; ++i) top = fmaxf(top, z[i]);
-            top = group_max<G>(top);
-            const bool low = use && sum < 1e-6f;
-            const float shift = top == -INFINITY ? 0.0f : top;
-            float ratios = 0.0f;
+            for (int u = 0; u < U; ++u) {
+                ratios[u] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4 * NV; ++i) {
-                const float r = ex2_approx((z[i] - shift) * kLog2e);
-                ratios += r;
-                if (low) {
-                    p[i] = r;
-                    if (m) m[i] = 1.0f;
+                for (int i = 0; i < N; ++i) {
+                    x[u][i] = ex2_approx((x[u][i] - top[u]) * kLog2e);
+                    ratios[u] += x[u][i];
                 }
             }
-            ratios = group_sum<G>(ratios);
-            if (low) sum = ratios;
+            group_sum<G>(ratios);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (use[u] && sum[u] < 1e-6f) {
+                    sum[u] = ratios[u];
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        z[u][i] = x[u][i];
+                        if constexpr (SLOPE) m[u][i] = 1.0f;
+                    }
+                }
+            }
         }
-#pragma unroll
-        for (int i = 0; i < 4 * NV; ++i) z[i] = p[i];
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-    for (int i = 0; i < 4 * NV; ++i) z[i] *= inv;
+    for (int u = 0; u < U; ++u) {
+        const float inv = sum[u] == 0.0f ? 0.0f : rcp_approx(sum[u]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[u][i] *= inv;
+    }
 }
 
 template <typename T, int G, int NV, bool SIGMOID>
-__global__ void __launch_bounds__(kThreads) balance_partial_kernel(const BalanceArgs a, const Plan p)
+__global__ void __launch_bounds__(kThreads, 4) balance_partial_kernel(const BalanceArgs a, const Plan p)
 {
     pdl_enter();
     __shared__ float red[kWarps][G * 4 * NV];
@@ -224,32 +284,25 @@ __global__ void __launch_bounds__(kThreads) balance_partial_kernel(const Balance
 #pragma unroll
         for (int i = 0; i < 4 * NV; ++i) sum[i] = 0.0f;
         int mine = 0;
-        for (int64_t n0 = lo; n0 < hi; n0 += GROUPS * kUnroll) {
-            float4 v[kUnroll][NV];
-            bool use[kUnroll];
+        constexpr int U = kForwardUnroll;
+        for (int64_t n0 = lo; n0 < hi; n0 += GROUPS * U) {
+            float z[U][4 * NV], none[1][4 * NV];
+            bool use[U];
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
+            for (int u = 0; u < U; ++u) {
                 const int64_t n = n0 + u * GROUPS + group;
                 use[u] = n < hi && (!a.mask || a.mask[n] != 0);
-#pragma unroll
-                for (int j = 0; j < NV; ++j)
-                    v[u][j] = use[u] ? load4<false>(logits + n * a.E, (j * G + q) * 4, a.E, vec)
-                                     : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-            }
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                float z[4 * NV];
-#pragma unroll
-                for (int j = 0; j < NV; ++j) {
-                    z[4 * j] = v[u][j].x;
-                    z[4 * j + 1] = v[u][j].y;
-                    z[4 * j + 2] = v[u][j].z;
-                    z[4 * j + 3] = v[u][j].w;
-                }
-                scores<G, NV, SIGMOID>(z, nullptr, use[u]);
                 mine += use[u] && q == 0;
+            }
+            auto load = [&](float (&x)[U][4 * NV]) {
+                load_tokens<false, G, NV>(x, logits, n0 + group, GROUPS, use, q, a.E, vec);
+            };
+            load(z);
+            scores<G, NV, SIGMOID, false>(z, none, use, load);
 #pragma unroll
-                for (int i = 0; i < 4 * NV; ++i) sum[i] += z[i];
+            for (int u = 0; u < U; ++u) {
+#pragma unroll
+                for (int i = 0; i < 4 * NV; ++i) sum[i] += z[u][i];
             }
         }
         const int64_t ids = (hi - lo) * a.k;
@@ -308,7 +361,7 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(const BalanceArgs 
     double P = 0.0;
     int n = 0, T = 0, odd = 0;
     if (e < a.E) {
-#pragma unroll 4
+#pragma unroll 8
         for (int64_t c = c0 + warp; c < c1; c += warps) {
             P += psum[(c + s) * a.E + e];
             n += cnt[(c + s) * a.E + e];
@@ -403,7 +456,7 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(const BalanceArgs 
 }
 
 template <typename T, int G, int NV, bool SIGMOID>
-__global__ void __launch_bounds__(kThreads) balance_backward_kernel(const BalanceArgs a, int64_t per_cta)
+__global__ void __launch_bounds__(kThreads, 4) balance_backward_kernel(const BalanceArgs a, int64_t per_cta)
 {
     pdl_enter();
     constexpr int GROUPS = kThreads / G;
@@ -418,20 +471,22 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(const Balanc
     float c[4 * NV];
 #pragma unroll
     for (int i = 0; i < 4 * NV; ++i) c[i] = 0.0f;
-    for (int64_t n0 = begin; n0 < end; n0 += GROUPS * kUnroll) {
-        float4 v[kUnroll][NV];
-        bool use[kUnroll];
+    constexpr int U = kBackwardUnroll;
+    for (int64_t n0 = begin; n0 < end; n0 += GROUPS * U) {
+        float z[U][4 * NV], m[SIGMOID ? U : 1][4 * NV];
+        bool use[U];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
+        for (int u = 0; u < U; ++u) {
             const int64_t n = n0 + u * GROUPS + group;
             use[u] = n < end && (!a.mask || a.mask[n] != 0);
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-                v[u][j] = use[u] ? load4<true>(logits + n * a.E, (j * G + q) * 4, a.E, vec)
-                                 : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
         }
+        auto load = [&](float (&x)[U][4 * NV]) {
+            load_tokens<true, G, NV>(x, logits, n0 + group, GROUPS, use, q, a.E, vec);
+        };
+        load(z);
+        scores<G, NV, SIGMOID, SIGMOID>(z, m, use, load);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
+        for (int u = 0; u < U; ++u) {
             const int64_t n = n0 + u * GROUPS + group;
             if (n < end) {
                 while (n >= hi && s + 1 < a.S) {
@@ -451,19 +506,10 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(const Balanc
                     c[i] = e < a.E ? w * static_cast<float>(__ldg(cs + e)) : 0.0f;
                 }
             }
-            float z[4 * NV], m[4 * NV];
+            float dot[1] = {0.0f};
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                z[4 * j] = v[u][j].x;
-                z[4 * j + 1] = v[u][j].y;
-                z[4 * j + 2] = v[u][j].z;
-                z[4 * j + 3] = v[u][j].w;
-            }
-            scores<G, NV, SIGMOID>(z, SIGMOID ? m : nullptr, use[u]);
-            float dot = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 4 * NV; ++i) dot = fmaf(z[i], c[i], dot);
-            dot = group_sum<G>(dot);
+            for (int i = 0; i < 4 * NV; ++i) dot[0] = fmaf(z[u][i], c[i], dot[0]);
+            group_sum<G>(dot);
             if (n >= end) continue;
             const bool real = use[u] && in;
             float *out = a.dlogits + n * a.E;
@@ -473,8 +519,8 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(const Balanc
                 float o[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float g = z[4 * j + i] * (c[4 * j + i] - dot);
-                    if (SIGMOID) g *= m[4 * j + i];
+                    float g = z[u][4 * j + i] * (c[4 * j + i] - dot[0]);
+                    if constexpr (SIGMOID) g *= m[u][4 * j + i];
                     o[i] = real ? g : 0.0f;
                 }
                 if (vec) {
@@ -529,9 +575,9 @@ cudaError_t launch_balance_loss(const BalanceArgs &a, cudaStream_t s)
     if (a.dtype == kF32) err = a.sigmoid ? forward<float, true>(a, p, s) : forward<float, false>(a, p, s);
     else err = a.sigmoid ? forward<__nv_bfloat16, true>(a, p, s) : forward<__nv_bfloat16, false>(a, p, s);
     if (err != cudaSuccess) return err;
-    // many chunks to a sequence: a warp each; few: no more warps than chunks
+    // four chunks of a sequence to a warp, as far as 32 warps go
     const int64_t each = p.chunks / a.S + 1;
-    const int warps = static_cast<int>(min64(32, max64(2, each)));
+    const int warps = static_cast<int>(min64(32, max64(2, each / 4)));
     const int64_t ctas = static_cast<int64_t>(a.S) * p.groups;
     if (ctas >= (static_cast<int64_t>(1) << 31)) return cudaErrorInvalidValue;
     return launch_k(balance_finish_kernel, dim3(static_cast<unsigned>(ctas)), dim3(32 * warps), 0, s, a, p);
