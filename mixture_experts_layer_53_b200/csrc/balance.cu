@@ -29,9 +29,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kForwardUnroll = 4, kBackwardUnroll = 2;  // tokens a lane group handles at once
+// Tokens a lane group handles at once; the next ones are on their way from
+// memory meanwhile.  (At E = 256, 131072 tokens of fp32: one token 47 us for
+// the gradient, two 52 us with more registers; the loss 46.9 and 44.9 us.)
+constexpr int kForwardUnroll = 2, kBackwardUnroll = 1;
 constexpr int kMinChunk = 32;
-constexpr int kMaxChunks = 1184;  // 148 SMs x 8 CTAs
+constexpr int kMaxChunks = 592;  // 148 SMs x 4 CTAs: one wave
 constexpr int kBadId = 1, kBadCut = 2;  // flags of a segment or sequence
 
 __host__ __device__ __forceinline__ int64_t align256(int64_t b) { return (b + 255) & ~static_cast<int64_t>(255); }
@@ -47,7 +50,7 @@ Plan make_plan(int64_t N, int E, int S)
 {
     Plan p{};
     const int64_t even = (N + kMaxChunks - 1) / kMaxChunks;
-    p.chunk = max64(kMinChunk, (even + 7) / 8 * 8);
+    p.chunk = max64(kMinChunk, (even + 15) / 16 * 16);
     p.chunks = max64(1, (N + p.chunk - 1) / p.chunk);
     p.slots = p.chunks + S;
     p.groups = (E + 31) / 32;
@@ -89,31 +92,76 @@ struct Seqs {
     }
 };
 
-// Four consecutive logits from expert e on; -inf past E.  The first pass
-// leaves them in L2 for the second (the gradient's), which reads them last.
-template <bool LAST, typename V> __device__ __forceinline__ V load_vec(const V *p)
+// Loads that stay where they are written: ahead of their use by a round.  The
+// first pass leaves the logits in L2 for the second (the gradient's), which
+// reads them last.
+template <bool LAST> __device__ __forceinline__ float4 load_vec(const float4 *p)
 {
-    return LAST ? __ldcs(p) : __ldg(p);
+    float4 v;
+    if (LAST)
+        asm volatile("ld.global.cs.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+    else
+        asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+    return v;
 }
-template <bool LAST> __device__ __forceinline__ float4 load4(const float *p, int e, int E, bool vec)
+template <bool LAST> __device__ __forceinline__ uint2 load_vec(const uint2 *p)
 {
-    const float ninf = -INFINITY;
-    if (vec) return e < E ? load_vec<LAST>(reinterpret_cast<const float4 *>(p + e)) : make_float4(ninf, ninf, ninf, ninf);
-    return make_float4(e < E ? p[e] : ninf, e + 1 < E ? p[e + 1] : ninf, e + 2 < E ? p[e + 2] : ninf,
-                       e + 3 < E ? p[e + 3] : ninf);
+    uint2 v;
+    if (LAST) asm volatile("ld.global.cs.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    else asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
 }
-template <bool LAST>
-__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p, int e, int E, bool vec)
-{
-    const float ninf = -INFINITY;
-    if (vec) {
-        if (e >= E) return make_float4(ninf, ninf, ninf, ninf);
-        const uint2 v = load_vec<LAST>(reinterpret_cast<const uint2 *>(p + e));
+
+// Four consecutive logits as loaded: fp32 values, or pairs of bf16.
+template <typename T> struct Raw;
+template <> struct Raw<float> {
+    float4 v;
+    __device__ __forceinline__ void none() { v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); }
+    template <bool LAST> __device__ __forceinline__ void load(const float *p) { v = load_vec<LAST>(reinterpret_cast<const float4 *>(p)); }
+    __device__ __forceinline__ void set(float a, float b, float c, float d) { v = make_float4(a, b, c, d); }
+    __device__ __forceinline__ float4 get() const { return v; }
+};
+template <> struct Raw<__nv_bfloat16> {
+    uint2 v;
+    __device__ __forceinline__ void none() { v = make_uint2(0xFF80FF80u, 0xFF80FF80u); }
+    template <bool LAST> __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = load_vec<LAST>(reinterpret_cast<const uint2 *>(p)); }
+    __device__ __forceinline__ void set(float a, float b, float c, float d) { v = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d)); }
+    __device__ __forceinline__ float4 get() const
+    {
         return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
                            __uint_as_float(v.y & 0xFFFF0000u));
     }
-    return make_float4(e < E ? to_f32(p[e]) : ninf, e + 1 < E ? to_f32(p[e + 1]) : ninf,
-                       e + 2 < E ? to_f32(p[e + 2]) : ninf, e + 3 < E ? to_f32(p[e + 3]) : ninf);
+};
+
+// This lane's experts of a token: NV times four consecutive ones; -inf past E
+// and for a token that is not used.
+template <typename T, int NV> using Row = Raw<T>[NV];
+template <bool LAST, int G, int NV, typename T>
+__device__ __forceinline__ void load_token(Row<T, NV> &r, const T *row, bool use, int q, int E, bool vec)
+{
+    const float ninf = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int e = (j * G + q) * 4;
+        r[j].none();
+        if (use && e < E) {
+            if (vec) r[j].template load<LAST>(row + e);
+            else
+                r[j].set(to_f32(row[e]), e + 1 < E ? to_f32(row[e + 1]) : ninf, e + 2 < E ? to_f32(row[e + 2]) : ninf,
+                         e + 3 < E ? to_f32(row[e + 3]) : ninf);
+        }
+    }
+}
+template <int NV, typename T> __device__ __forceinline__ void unpack(float (&z)[4 * NV], const Row<T, NV> &r)
+{
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const float4 v = r[j].get();
+        z[4 * j] = v.x;
+        z[4 * j + 1] = v.y;
+        z[4 * j + 2] = v.z;
+        z[4 * j + 3] = v.w;
+    }
 }
 
 // U values summed (or their maxima taken) over the G lanes of a group, the
@@ -145,53 +193,30 @@ __device__ __forceinline__ float min_nan(float a, float b)
     return r;
 }
 
-// The logits of U tokens (those at n0 + u * stride + group that are `use`d),
-// this lane's 4 NV experts of each; -inf where there is none.
-template <bool LAST, int G, int NV, int U, typename T>
-__device__ __forceinline__ void load_tokens(float (&z)[U][4 * NV], const T *logits, int64_t n, int64_t stride,
-                                            const bool (&use)[U], int q, int E, bool vec)
-{
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-            if (use[u]) v = load4<LAST>(logits + (n + u * stride) * E, (j * G + q) * 4, E, vec);
-            z[u][4 * j] = v.x;
-            z[u][4 * j + 1] = v.y;
-            z[u][4 * j + 2] = v.z;
-            z[u][4 * j + 3] = v.w;
-        }
-    }
-}
-
 // Normalised scores of U tokens in place of their logits z; with SLOPE also m
 // = 1 - sigmoid(z).  Every lane of the warp takes part.  A token whose logits
 // are all -inf (or that is not used) has p = 0.  The exponent is the rounded
 // product of z - max (or z) and log2 e, so its error is relative to it: about
 // 1e-7 for the scores that matter, 6e-8 |z - max| for small ones.  `again`
-// loads the logits once more, for the rare path that needs them.
+// loads token u's logits once more, for the rare path that needs them.
 template <int G, int NV, bool SIGMOID, bool SLOPE, int U, typename Again>
 __device__ __forceinline__ void scores(float (&z)[U][4 * NV], float (&m)[SLOPE ? U : 1][4 * NV], const bool (&use)[U],
                                        Again &&again)
 {
     constexpr int N = 4 * NV;
-    float sum[U], top[U];
-    auto tops = [&](const float (&x)[U][N]) {
+    float sum[U];
+    if constexpr (!SIGMOID) {
+        float top[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             top[u] = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < N; ++i) top[u] = fmaxf(top[u], x[u][i]);
+            for (int i = 0; i < N; ++i) top[u] = fmaxf(top[u], z[u][i]);
         }
         group_max<G>(top);
 #pragma unroll
-        for (int u = 0; u < U; ++u) top[u] = top[u] == -INFINITY ? 0.0f : top[u];
-    };
-    if constexpr (!SIGMOID) {
-        tops(z);
-#pragma unroll
         for (int u = 0; u < U; ++u) {
+            top[u] = top[u] == -INFINITY ? 0.0f : top[u];
             sum[u] = 0.0f;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
@@ -216,36 +241,29 @@ __device__ __forceinline__ void scores(float (&z)[U][4 * NV], float (&m)[SLOPE ?
             }
         }
         group_sum<G>(sum);
-        bool low = false;
 #pragma unroll
-        for (int u = 0; u < U; ++u) low |= use[u] && sum[u] < 1e-6f;
-        if (__any_sync(0xffffffffu, low)) {
+        for (int u = 0; u < U; ++u) {
+            const bool low = use[u] && sum[u] < 1e-6f;
+            if (!__any_sync(0xffffffffu, low)) continue;
             // Every logit of a token is far below zero: the sigmoids underflow
             // but their ratios, those of e^z, do not.
-            float x[U][N], ratios[U];
-            again(x);
-            tops(x);
+            float x[N], top[1] = {-INFINITY}, ratios[1] = {0.0f};
+            again(x, u);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                ratios[u] = 0.0f;
+            for (int i = 0; i < N; ++i) top[0] = fmaxf(top[0], x[i]);
+            group_max<G>(top);
+            if (top[0] == -INFINITY) top[0] = 0.0f;
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    x[u][i] = ex2_approx((x[u][i] - top[u]) * kLog2e);
-                    ratios[u] += x[u][i];
+            for (int i = 0; i < N; ++i) {
+                x[i] = ex2_approx((x[i] - top[0]) * kLog2e);
+                ratios[0] += x[i];
+                if (low) {
+                    z[u][i] = x[i];
+                    if constexpr (SLOPE) m[u][i] = 1.0f;
                 }
             }
             group_sum<G>(ratios);
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (use[u] && sum[u] < 1e-6f) {
-                    sum[u] = ratios[u];
-#pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        z[u][i] = x[u][i];
-                        if constexpr (SLOPE) m[u][i] = 1.0f;
-                    }
-                }
-            }
+            if (low) sum[u] = ratios[0];
         }
     }
 #pragma unroll
@@ -285,32 +303,60 @@ __global__ void __launch_bounds__(kThreads, 4) balance_partial_kernel(const Bala
         for (int i = 0; i < 4 * NV; ++i) sum[i] = 0.0f;
         int mine = 0;
         constexpr int U = kForwardUnroll;
+        Row<T, NV> next[U];
+        bool used[U];
+        auto load = [&](Row<T, NV> &r, int64_t n, bool use) {
+            load_token<false, G, NV>(r, logits + n * a.E, use, q, a.E, vec);
+        };
+        auto fetch = [&](int64_t n0) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t n = n0 + u * GROUPS + group;
+                used[u] = n < hi && (!a.mask || a.mask[n] != 0);
+                load(next[u], n, used[u]);
+            }
+        };
+        fetch(lo);
+        // counts, several ids of a thread on their way at once
+        constexpr int IDS = 8;
+        const int64_t ids = (hi - lo) * a.k;
+        for (int64_t i0 = threadIdx.x; i0 < ids; i0 += kThreads * IDS) {
+            int e[IDS];
+            bool count[IDS];
+#pragma unroll
+            for (int i = 0; i < IDS; ++i) {
+                const int64_t at = i0 + i * kThreads;
+                count[i] = at < ids;
+                e[i] = count[i] ? __ldg(a.ids + lo * a.k + at) : 0;
+                if (a.mask && count[i]) count[i] = a.mask[lo + static_cast<int>(at) / a.k] != 0;
+            }
+#pragma unroll
+            for (int i = 0; i < IDS; ++i) {
+                if (!count[i]) continue;
+                if (static_cast<unsigned>(e[i]) < static_cast<unsigned>(a.E)) atomicAdd(&cnt[e[i]], 1);
+                else bad = kBadId;
+            }
+        }
         for (int64_t n0 = lo; n0 < hi; n0 += GROUPS * U) {
             float z[U][4 * NV], none[1][4 * NV];
             bool use[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int64_t n = n0 + u * GROUPS + group;
-                use[u] = n < hi && (!a.mask || a.mask[n] != 0);
+                use[u] = used[u];
                 mine += use[u] && q == 0;
+                unpack<NV, T>(z[u], next[u]);
             }
-            auto load = [&](float (&x)[U][4 * NV]) {
-                load_tokens<false, G, NV>(x, logits, n0 + group, GROUPS, use, q, a.E, vec);
-            };
-            load(z);
-            scores<G, NV, SIGMOID, false>(z, none, use, load);
+            fetch(n0 + GROUPS * U);
+            scores<G, NV, SIGMOID, false>(z, none, use, [&](float (&x)[4 * NV], int u) {
+                Row<T, NV> r;
+                load(r, n0 + u * GROUPS + group, use[u]);
+                unpack<NV, T>(x, r);
+            });
 #pragma unroll
             for (int u = 0; u < U; ++u) {
 #pragma unroll
                 for (int i = 0; i < 4 * NV; ++i) sum[i] += z[u][i];
             }
-        }
-        const int64_t ids = (hi - lo) * a.k;
-        for (int64_t i = threadIdx.x; i < ids; i += kThreads) {
-            if (a.mask && a.mask[lo + i / a.k] == 0) continue;
-            const int e = a.ids[lo * a.k + i];
-            if (static_cast<unsigned>(e) < static_cast<unsigned>(a.E)) atomicAdd(&cnt[e], 1);
-            else bad = kBadId;
         }
         if (mine) atomicAdd(&valid, mine);
         // over the warp's lane groups, then over the warps
@@ -472,19 +518,34 @@ __global__ void __launch_bounds__(kThreads, 4) balance_backward_kernel(const Bal
 #pragma unroll
     for (int i = 0; i < 4 * NV; ++i) c[i] = 0.0f;
     constexpr int U = kBackwardUnroll;
+    Row<T, NV> next[U];
+    bool used[U];
+    auto load = [&](Row<T, NV> &r, int64_t n, bool use) {
+        load_token<true, G, NV>(r, logits + n * a.E, use, q, a.E, vec);
+    };
+    auto fetch = [&](int64_t n0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t n = n0 + u * GROUPS + group;
+            used[u] = n < end && (!a.mask || a.mask[n] != 0);
+            load(next[u], n, used[u]);
+        }
+    };
+    fetch(begin);
     for (int64_t n0 = begin; n0 < end; n0 += GROUPS * U) {
         float z[U][4 * NV], m[SIGMOID ? U : 1][4 * NV];
         bool use[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t n = n0 + u * GROUPS + group;
-            use[u] = n < end && (!a.mask || a.mask[n] != 0);
+            use[u] = used[u];
+            unpack<NV, T>(z[u], next[u]);
         }
-        auto load = [&](float (&x)[U][4 * NV]) {
-            load_tokens<true, G, NV>(x, logits, n0 + group, GROUPS, use, q, a.E, vec);
-        };
-        load(z);
-        scores<G, NV, SIGMOID, SIGMOID>(z, m, use, load);
+        fetch(n0 + GROUPS * U);
+        scores<G, NV, SIGMOID, SIGMOID>(z, m, use, [&](float (&x)[4 * NV], int u) {
+            Row<T, NV> r;
+            load(r, n0 + u * GROUPS + group, use[u]);
+            unpack<NV, T>(x, r);
+        });
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t n = n0 + u * GROUPS + group;
