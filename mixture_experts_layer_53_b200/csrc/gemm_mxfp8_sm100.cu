@@ -11,7 +11,7 @@
 // spends more time on it than the tensor core on the products).
 //
 // The weights are the MMA's M operand and the rows its N operand: a tile is
-// 256 weight rows (two accumulators of 128) by up to NMAX of the expert's
+// 128 weight rows for each of its accumulators by up to NMAX of the expert's
 // rows, and the MMA's N is the rows that the tile really has, rounded up to
 // 16.  So a ragged slice costs what its rows cost (with the rows as M, a
 // slice of 129 rows cost as much as one of 256), a slice of up to NMAX rows
@@ -20,16 +20,20 @@
 // Tile list (expert, weight tile, row tile), row tiles innermost: CTAs that
 // run at the same time share an expert's weight tile through L2.
 //
-// Two shapes.  BIG: NMAX = 240, one set of accumulators (480 TMEM columns) --
-// 31% fewer bytes from L2 per product than 128 x 256 tiles; its epilogue
-// holds the tile in registers, so the next tile's MMAs wait for the TMEM
-// reads only.  Else NMAX = 112 and two sets, so that the epilogue overlaps
-// the next tile: slices of few rows, and epilogues that cannot hold a BIG tile
-// (fp32 results, GELU's 240 values a thread).
+// Where arithmetic bounds it, it is shared memory that does: an MMA of N rows
+// takes N / 2 cycles and reads 4 KB of weights and 32 N bytes of rows.  Three
+// shapes share the 512 TMEM columns:
+//   two accumulators of 240 rows: fewest bytes from L2 and shared memory per
+//     product.  Its epilogue holds the tile in registers, so that the next
+//     tile's MMAs wait for the TMEM reads only.
+//   one accumulator of 240 rows, twice: for epilogues that cannot hold two (fp32
+//     results, GELU); they overlap the next tile's MMAs.
+//   two of 112 rows, twice: slices of few rows, bound by reading weights.  Four
+//     stages instead of three, and an epilogue that overlaps.
 //
 // Warp roles (384 threads, one CTA per SM, persistent):
-//   warp 0      TMA producer: per k-block of 128 values W (32 KB) and the
-//               tile's rows, in boxes of 128, 64, 32 and 16 rows
+//   warp 0      TMA producer: per k-block of 128 values W (16 KB for each
+//               accumulator) and the tile's rows, in boxes of 128, 64, 32 and 16
 //   warp 1      allocates TMEM; one lane issues the MMAs (K = 32), four to a
 //               k-block and accumulator
 //   warps 2, 3  scales of 128 rows each (and the weights'): pack four
@@ -37,8 +41,9 @@
 //               [row / 32] order that tcgen05.cp spreads over the TMEM lanes;
 //               the next group's scales are on their way meanwhile
 //   warps 4-11  epilogue: a warp owns 32 weight rows (its TMEM lane quarter)
-//               of one accumulator, or with SwiGLU (gate and up of the same
-//               128 hidden units in the two) every other 32 rows of both
+//               of one of two accumulators, or every other 32 rows: of the
+//               one, or with SwiGLU of both (gate and up of the same 128
+//               hidden units)
 //
 // SwiGLU and GELU: the 128 hidden units of an accumulator are one scale block
 // of h; the largest |h| of a row is reduced over the lanes and, through
@@ -58,33 +63,42 @@ using namespace fp8;
 constexpr int ROLE_REGS = 88, SUM_REGS = 208;
 static_assert(32 * FIRST_SUM_WARP * ROLE_REGS + 32 * SUM_WARPS * SUM_REGS <= THREADS * LAUNCH_REGS, "register split");
 constexpr int WM = 128;                      // weight rows of an accumulator
-constexpr int W_BYTES = 2 * WM * BK;
 constexpr int GROUP = 4;                     // k-blocks of one scale word
 constexpr int SLOTS = 4;                     // groups of scales in shared memory
+constexpr int AHEAD = 4;                     // groups whose fp32 scales are on their way
 constexpr int SCALE_BYTES = 4 * 512;         // W's two accumulators, rows 0-127 and 128-255
 constexpr uint32_t TMEM_COLS = 512;
 
-template <bool BIG> struct Shape {
-    static constexpr int NMAX = BIG ? 240 : 112;
-    static constexpr int BUFS = BIG ? 1 : 2;
-    static constexpr int ATOMS = BIG ? 2 : 1;      // 128-row scale tiles of the rows
+// A tile: accumulators of WM weight rows, their most rows, sets of them.
+template <int ACC_, int NMAX_, int BUFS_> struct Shape {
+    static constexpr int ACC = ACC_, NMAX = NMAX_, BUFS = BUFS_;
+    static constexpr int ATOMS = NMAX > 128 ? 2 : 1;  // 128-row scale tiles of the rows
+    static constexpr int W_BYTES = ACC * WM * BK;
     static constexpr int STAGE = W_BYTES + NMAX * BK;
-    static constexpr int STAGES = BIG ? 3 : 4;
-    static constexpr uint32_t SCALE_COL = 2 * BUFS * NMAX;  // per slot of two: 8 columns of W, 4 per atom
-    static constexpr uint32_t SLOT_COLS = 8 + 4 * ATOMS;
+    static constexpr int STAGES = STAGE > 48 * 1024 ? 3 : 4;
+    static constexpr uint32_t SCALE_COL = ACC * BUFS * NMAX;
+    static constexpr uint32_t SLOT_COLS = 4 * ACC + 4 * ATOMS;  // of the weights, of the rows; two slots
     static_assert(SCALE_COL + 2 * SLOT_COLS <= TMEM_COLS, "TMEM columns");
     static_assert(STAGE % 1024 == 0, "swizzled tiles start on 1024 bytes");
+    static_assert(NMAX % 16 == 0, "the MMA's N");
 };
+using Wide = Shape<2, 240, 1>;
+using Tall = Shape<1, 240, 2>;
+using Few = Shape<2, 112, 2>;
+constexpr int kFewRows = 80;  // average rows of a slice up to which Few is taken
 
 struct RowMaps {
     CUtensorMap box[4];  // 128, 64, 32, 16 rows
 };
 
-template <bool BIG> struct Ctl {
+template <typename S> struct Ctl {
     alignas(128) uint8_t scales[SLOTS][SCALE_BYTES];
+    // fp32 scales on their way: per scale warp and group, 17 values a lane
+    // (written and read by the same lane)
+    float ahead[S::ATOMS][AHEAD][4 * GROUP + 1][32];
     uint32_t amax[2][2][4][128];  // [phase][half][lane quarter][the half's rows]
-    uint64_t full[Shape<BIG>::STAGES];
-    uint64_t empty[Shape<BIG>::STAGES];
+    uint64_t full[S::STAGES];
+    uint64_t empty[S::STAGES];
     uint64_t sfull[SLOTS];
     uint64_t sempty[SLOTS];
     uint64_t tfull[2];
@@ -96,8 +110,9 @@ template <bool BIG> struct Ctl {
     Slices slices;
 };
 
-template <bool BIG> constexpr size_t smem_bytes() { return 1024 + Shape<BIG>::STAGES * Shape<BIG>::STAGE + sizeof(Ctl<BIG>); }
-static_assert(smem_bytes<false>() <= 232448 && smem_bytes<true>() <= 232448, "shared memory per CTA");
+template <typename S> constexpr size_t smem_bytes() { return 1024 + S::STAGES * S::STAGE + sizeof(Ctl<S>); }
+static_assert(smem_bytes<Wide>() <= 232448 && smem_bytes<Tall>() <= 232448 && smem_bytes<Few>() <= 232448,
+              "shared memory per CTA");
 
 // Instruction descriptor of kind::mxf8f6f4: A and B e4m3 (0) and K-major, N >> 3
 // at [17,23), UE8M0 scales (bit 23), M >> 4 at [24,29); the byte of the scale
@@ -138,12 +153,22 @@ __device__ __forceinline__ uint64_t desc_scales(uint32_t smem_addr)
     return d;
 }
 
-// A load that stays where it is written: ahead of its use by a group.
-__device__ __forceinline__ float load_ahead(const float *p)
+// A copy of four bytes to shared memory that nobody waits for yet.
+__device__ __forceinline__ void copy_ahead(float *dst, const float *src)
 {
-    float v;
-    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
-    return v;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until all but this thread's last N groups of copies have landed.
+template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// A predicated 4-byte store (a branch around a plain one costs the unrolled
+// epilogues up to a third of their time).
+__device__ __forceinline__ void store_if(bool p, void *dst, uint32_t v)
+{
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %0, 0;\n\t@q st.global.b32 [%1], %2;\n\t}\n" ::"r"(static_cast<int>(p)),
+                 "l"(dst), "r"(v)
+                 : "memory");
 }
 
 // Four lanes hold a column each, of the same four rows (a byte per row): lane
@@ -156,19 +181,19 @@ __device__ __forceinline__ uint32_t transpose4(uint32_t w, int lane)
     return __byte_perm(w, z, lane & 2 ? 0x3276u : 0x5410u);
 }
 
-template <int EPI, bool BIG>
+template <int EPI, typename S>
 __global__ void __launch_bounds__(THREADS, 1)
     ffn_gemm_mxfp8_kernel(const __grid_constant__ RowMaps tmA, const __grid_constant__ CUtensorMap tmW,
                           const __grid_constant__ CUtensorMap tmW3, const GemmArgs g)
 {
-    using S = Shape<BIG>;
     constexpr bool kHidden = EPI == EPI_SWIGLU || EPI == EPI_GELU;
-    static_assert(!BIG || EPI == EPI_SWIGLU || EPI == EPI_BF16, "a BIG tile fits the epilogue's registers");
-    pdl_enter();
+    // the epilogue's halves: an accumulator each, or every other 32 rows
+    constexpr bool kHalfAcc = S::ACC == 2 && EPI != EPI_SWIGLU;
+    static_assert(EPI == EPI_BF16 || S::ACC == (EPI == EPI_SWIGLU ? 2 : 1), "a tile fits the epilogue's registers");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *tiles = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                  ~static_cast<uintptr_t>(1023));
-    Ctl<BIG> *ctl = reinterpret_cast<Ctl<BIG> *>(tiles + S::STAGES * S::STAGE);
+    Ctl<S> *ctl = reinterpret_cast<Ctl<S> *>(tiles + S::STAGES * S::STAGE);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int *abort_flag = &ctl->abort;
 
@@ -199,6 +224,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         tmem_alloc(&ctl->tmem_base, TMEM_COLS);
         tmem_relinquish();
     }
+    // nothing above touches memory that an earlier kernel writes
+    pdl_enter();
     tc_fence_before();
     load_slices<S::NMAX>(&ctl->slices, g);
     tc_fence_after();
@@ -207,7 +234,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tmem_base = ctl->tmem_base;
     const int total = sl->mt[g.E] * g.n_tiles;
     const int num_kb = (g.K + BK - 1) / BK;
-    constexpr int TILE_N = EPI == EPI_SWIGLU ? WM : 2 * WM;  // result columns of a tile
+    constexpr int TILE_N = EPI == EPI_SWIGLU ? WM : S::ACC * WM;  // result columns of a tile
     // A slice's rows in tiles of equal size (a multiple of 16): the tiles of a
     // wave then take equally long.
     struct Rows {
@@ -235,9 +262,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                         ok = false;
                         break;
                     }
-                    uint8_t *sW = tiles + stage * S::STAGE, *sA = sW + W_BYTES;
+                    uint8_t *sW = tiles + stage * S::STAGE, *sA = sW + S::W_BYTES;
                     uint64_t *full = &ctl->full[stage];
-                    mbar_arrive_expect_tx(full, static_cast<uint32_t>(W_BYTES + n * BK));
+                    mbar_arrive_expect_tx(full, static_cast<uint32_t>(S::W_BYTES + n * BK));
                     armed |= 1u << stage;
                     armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
                     tma_load_3d(sW, &tmW, full, kb * BK, n0, ti.e);
@@ -271,10 +298,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
                 const Tile ti = decode_tile(t, sl, g.E, g.n_tiles);
                 const int n = (rows_of(ti).count + 15) & ~15;
-                const bool both = EPI == EPI_SWIGLU || ti.n_tile * TILE_N + WM < g.n_out;
+                const bool both = S::ACC == 2 && (EPI == EPI_SWIGLU || ti.n_tile * TILE_N + WM < g.n_out);
                 if (!mbar_wait(&ctl->tempty[buf], tphase ^ 1u, abort_flag, g.status)) break;
                 tc_fence_after();
-                const uint32_t d = tmem_base + static_cast<uint32_t>(buf * 2 * S::NMAX);
+                const uint32_t d = tmem_base + static_cast<uint32_t>(buf * S::ACC * S::NMAX);
                 for (int kb0 = 0; kb0 < num_kb && ok; kb0 += GROUP) {
                     // The group's scales are there, and the MMAs of the
                     // group before the last, which read the same TMEM
@@ -287,12 +314,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sw = tmem_base + S::SCALE_COL + (group & 1u) * S::SLOT_COLS, sr = sw + 8u;
+                    const uint32_t sw = tmem_base + S::SCALE_COL + (group & 1u) * S::SLOT_COLS, sr = sw + 4u * S::ACC;
                     const uint32_t src = smem_u32(ctl->scales[slot]);
                     copy_scales(sw, desc_scales(src));
-                    copy_scales(sw + 4u, desc_scales(src + 512));
+                    if (S::ACC == 2) copy_scales(sw + 4u, desc_scales(src + 512));
                     copy_scales(sr, desc_scales(src + 1024));
-                    if (BIG) copy_scales(sr + 4u, desc_scales(src + 1536));
+                    if (S::ATOMS == 2) copy_scales(sr + 4u, desc_scales(src + 1536));
                     issued = true;
                     const int kbs = min(GROUP, num_kb - kb0);
                     for (int j = 0; j < kbs; ++j) {
@@ -301,7 +328,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t w_addr = smem_u32(tiles + stage * S::STAGE), a_addr = w_addr + W_BYTES;
+                        const uint32_t w_addr = smem_u32(tiles + stage * S::STAGE), a_addr = w_addr + S::W_BYTES;
                         const uint32_t idesc = idesc_mxf8(n, j), add = (kb0 | j) != 0 ? 1u : 0u;
 #pragma unroll
                         for (int kk = 0; kk < BK / 32; ++kk)
@@ -340,82 +367,88 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int atom = warp - 2;
             const int nblocks = (g.n_out + kFp8Block - 1) / kFp8Block;
             bool odd_scale = false;
-            // a group of k-blocks and its values on their way from memory
-            struct Fetch {
-                int t, kb0;
-                float a[4][GROUP];  // rows lane, lane + 32, ... of four k-blocks
-                float w;            // lanes 0-3, 4-7: the two accumulators' weights
-                uint32_t rows;      // bit i: row i of this lane is in the tile
-            };
+            // Copies of a group's values on their way: rows lane, lane + 32,
+            // ... of four k-blocks; lanes 0-3 and 4-7: the two accumulators'
+            // weights.  1 where there is none.
             Tile ti{};
-            int decoded = -1;
-            auto fetch = [&](Fetch &f) {
-                if (f.t >= total) return;
-                if (decoded != f.t) ti = decode_tile(f.t, sl, g.E, g.n_tiles);
-                decoded = f.t;
-                const Rows tr = rows_of(ti);
-                const int row0 = tr.first, rows = tr.count;
-                f.rows = 0;
+            Rows tr{};
+            int t_ahead = blockIdx.x, kb_ahead = 0, decoded = -1;
+            auto fetch = [&](float (&to)[4 * GROUP + 1][32]) {
+                if (t_ahead < total) {
+                    if (decoded != t_ahead) {
+                        ti = decode_tile(t_ahead, sl, g.E, g.n_tiles);
+                        tr = rows_of(ti);
+                        decoded = t_ahead;
+                    }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = atom * 128 + 32 * i + lane;
-                    f.rows |= (r < rows ? 1u : 0u) << i;
-                    const float *p = g.a_scales + row0 + r + static_cast<int64_t>(f.kb0) * g.rows;
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = atom * 128 + 32 * i + lane;
+                        const float *p = g.a_scales + tr.first + r + static_cast<int64_t>(kb_ahead) * g.rows;
 #pragma unroll
-                    for (int j = 0; j < GROUP; ++j)
-                        f.a[i][j] = r < rows && f.kb0 + j < num_kb ? load_ahead(p + static_cast<int64_t>(j) * g.rows) : 1.0f;
+                        for (int j = 0; j < GROUP; ++j) {
+                            float *dst = &to[i * GROUP + j][lane];
+                            if (r < tr.count && kb_ahead + j < num_kb) copy_ahead(dst, p + static_cast<int64_t>(j) * g.rows);
+                            else *dst = 1.0f;
+                        }
+                    }
+                    const int j = kb_ahead + (lane & 3), h = lane >> 2 & 1;
+                    const int nb = EPI == EPI_SWIGLU ? ti.n_tile : min(ti.n_tile * S::ACC + h, nblocks - 1);
+                    const float *p = (EPI == EPI_SWIGLU && h ? g.w3_scales : g.w_scales) +
+                                     (static_cast<int64_t>(ti.e) * nblocks + nb) * num_kb;
+                    float *dst = &to[4 * GROUP][lane];
+                    if (atom == 0 && lane < 8 && j < num_kb) copy_ahead(dst, p + j);
+                    else *dst = 1.0f;
                 }
-                const int j = f.kb0 + (lane & 3), h = lane >> 2 & 1;
-                const int nb = EPI == EPI_SWIGLU ? ti.n_tile : min(ti.n_tile * 2 + h, nblocks - 1);
-                const float *p = (EPI == EPI_SWIGLU && h ? g.w3_scales : g.w_scales) +
-                                 (static_cast<int64_t>(ti.e) * nblocks + nb) * num_kb;
-                f.w = atom == 0 && j < num_kb ? load_ahead(p + j) : 1.0f;
+                copy_commit();
+                if ((kb_ahead += GROUP) >= num_kb) {
+                    kb_ahead = 0;
+                    t_ahead += gridDim.x;
+                }
             };
             // exponent codes; a scale that is no power of two (zero,
             // negative, any mantissa) is reported
-            auto code = [&](float v, bool counts) {
+            auto code = [&](float v) {
                 const uint32_t b = __float_as_uint(v), e = b >> 23;
-                odd_scale |= counts && (e == 0 || e > 255 || (e < 255 && (b & 0x7FFFFFu) != 0));
+                odd_scale |= e == 0 || e > 255 || (e < 255 && (b & 0x7FFFFFu) != 0);
                 return e & 255u;
             };
-            Fetch now, then;
-            now.t = blockIdx.x;
-            now.kb0 = 0;
-            fetch(now);
-            for (uint32_t group = 0; now.t < total; ++group) {
-                then.t = now.t;
-                then.kb0 = now.kb0 + GROUP;
-                if (then.kb0 >= num_kb) {
-                    then.kb0 = 0;
-                    then.t += gridDim.x;
-                }
-                fetch(then);
-                uint32_t w[4];
+            for (int i = 0; i + 1 < AHEAD; ++i) fetch(ctl->ahead[atom][i]);
+            uint32_t group = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+                for (int kb0 = 0; kb0 < num_kb; kb0 += GROUP, ++group) {
+                    fetch(ctl->ahead[atom][(group + AHEAD - 1) % AHEAD]);
+                    copy_wait<AHEAD - 1>();
+                    const float(&a)[4 * GROUP + 1][32] = ctl->ahead[atom][group % AHEAD];
+                    uint32_t w[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    w[i] = 0;
+                    for (int i = 0; i < 4; ++i) {
+                        w[i] = 0;
 #pragma unroll
-                    for (int j = 0; j < GROUP; ++j) w[i] |= code(now.a[i][j], now.rows >> i & 1u) << (8 * j);
+                        for (int j = 0; j < GROUP; ++j) w[i] |= code(a[i * GROUP + j][lane]) << (8 * j);
+                    }
+                    uint32_t e = code(a[4 * GROUP][lane]) << (8 * (lane & 3));
+                    e |= __shfl_xor_sync(0xffffffffu, e, 1);
+                    e |= __shfl_xor_sync(0xffffffffu, e, 2);
+                    const uint32_t w0 = __shfl_sync(0xffffffffu, e, 0), w1 = __shfl_sync(0xffffffffu, e, 4);
+                    const uint32_t slot = group % SLOTS;
+                    if (!__all_sync(0xffffffffu,
+                                    mbar_wait(&ctl->sempty[slot], (group / SLOTS & 1u) ^ 1u, abort_flag, g.status))) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *dst = ctl->scales[slot] + lane * 16;
+                    st16(dst + 1024 + 512 * atom, make_uint4(w[0], w[1], w[2], w[3]));
+                    if (atom == 0) {
+                        st16(dst, make_uint4(w0, w0, w0, w0));
+                        st16(dst + 512, make_uint4(w1, w1, w1, w1));
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl->sfull[slot]);
                 }
-                uint32_t e = code(now.w, true) << (8 * (lane & 3));
-                e |= __shfl_xor_sync(0xffffffffu, e, 1);
-                e |= __shfl_xor_sync(0xffffffffu, e, 2);
-                const uint32_t w0 = __shfl_sync(0xffffffffu, e, 0), w1 = __shfl_sync(0xffffffffu, e, 4);
-                const uint32_t slot = group % SLOTS;
-                if (!__all_sync(0xffffffffu,
-                                mbar_wait(&ctl->sempty[slot], (group / SLOTS & 1u) ^ 1u, abort_flag, g.status)))
-                    break;
-                uint8_t *dst = ctl->scales[slot] + lane * 16;
-                st16(dst + 1024 + 512 * atom, make_uint4(w[0], w[1], w[2], w[3]));
-                if (atom == 0) {
-                    st16(dst, make_uint4(w0, w0, w0, w0));
-                    st16(dst + 512, make_uint4(w1, w1, w1, w1));
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->sfull[slot]);
-                now = then;
             }
+            copy_wait<0>();  // none of this thread's copies is left behind
             if (odd_scale) set_status(g.status, kDevBadArgument);
         }
     } else {
@@ -432,7 +465,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!__all_sync(0xffffffffu, mbar_wait(&ctl->tfull[buf], tphase, abort_flag, g.status))) break;
             tc_fence_after();
             const uint32_t tbase =
-                tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(buf * 2 * S::NMAX);
+                tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(buf * S::ACC * S::NMAX) +
+                (kHalfAcc ? static_cast<uint32_t>(half * S::NMAX) : 0u);
             // this warp's loads from TMEM have completed
             auto release = [&] {
                 tc_fence_before();
@@ -444,20 +478,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             };
             // the first of this warp's 32 result columns, and this lane's
-            const int col0 = ti.n_tile * TILE_N + (EPI == EPI_SWIGLU ? 0 : half * WM) + quarter * 32, col = col0 + lane;
+            const int col0 = ti.n_tile * TILE_N + (kHalfAcc ? half * WM : 0) + quarter * 32, col = col0 + lane;
+            // this warp's chunks of 32 rows
+            constexpr int CH = (S::NMAX + (kHalfAcc ? 31 : 63)) / (kHalfAcc ? 32 : 64);
+            auto first_row = [&](int i) { return kHalfAcc ? 32 * i : 64 * i + 32 * half; };
             float bias = 0.0f;
             if (EPI != EPI_SWIGLU && g.bias && col < g.n_out)
                 bias = to_f32(g.bias[static_cast<int64_t>(ti.e) * g.n_out + col]);
 
             if constexpr (kHidden) {
-                // The half's chunks of 32 rows: SwiGLU every other one of
-                // the tile's, GELU (a scale block per half) all of them.
-                constexpr int CH = EPI == EPI_GELU ? 4 : BIG ? 4 : 2;
-                auto first_row = [&](int i) { return EPI == EPI_GELU ? 32 * i : 64 * i + 32 * half; };
-                if (EPI == EPI_GELU && ti.n_tile * TILE_N + half * WM >= g.n_out) {
-                    release();
-                    continue;
-                }
                 float h[CH][32];
                 uint32_t m[CH];  // lane j: the largest |h| of the chunk's row j over this warp's lanes
 #pragma unroll
@@ -472,7 +501,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         tmem_ld_wait(v);
                         tmem_ld_wait(up);
                     } else {
-                        tmem_ld32(tbase + half * S::NMAX + r0, v);
+                        tmem_ld32(tbase + r0, v);
                         tmem_ld_wait(v);
                     }
 #pragma unroll
@@ -495,7 +524,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (lane == 0) mbar_arrive(&ctl->there[half]);
                 if (!__all_sync(0xffffffffu, mbar_wait(&ctl->there[half], xphase, abort_flag, g.status))) break;
                 uint8_t *out = static_cast<uint8_t *>(g.out);
-                const int block = EPI == EPI_SWIGLU ? ti.n_tile : ti.n_tile * 2 + half;
 #pragma unroll
                 for (int i = 0; i < CH; ++i) {
                     const int r0 = first_row(i);
@@ -504,7 +532,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int q = 0; q < 4; ++q) m[i] = max(m[i], ctl->amax[xphase][half][q][32 * i + lane]);
                     const float2 s = fp8_scale(m[i]);
                     if (quarter == 0 && r0 + lane < rows)
-                        g.h_scales[static_cast<int64_t>(block) * g.rows + row0 + r0 + lane] = s.x;
+                        g.h_scales[static_cast<int64_t>(ti.n_tile) * g.rows + row0 + r0 + lane] = s.x;
                     uint8_t *at = out + (row0 + r0 + (lane & 3)) * g.n_out + col0 + (lane & ~3);
                     const int left = col0 + (lane & ~3) < g.n_out ? rows - r0 - (lane & 3) : 0;
 #pragma unroll
@@ -513,70 +541,65 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                         for (int u = 0; u < 4; ++u) x[u] = h[i][j + u] * __shfl_sync(0xffffffffu, s.y, j + u);
                         const uint32_t w = transpose4(cvt_e4m3x4(x[0], x[1], x[2], x[3]), lane);
-                        if (left > j) *reinterpret_cast<uint32_t *>(at) = w;
+                        store_if(left > j, at, w);
                         at += 4 * static_cast<int64_t>(g.n_out);
                     }
                 }
                 xphase ^= 1u;
             } else {
-                const uint32_t acc = tbase + static_cast<uint32_t>(half * S::NMAX);
                 if (col0 >= g.n_out) {
                     release();
                     continue;
                 }
-                constexpr int CH = (S::NMAX + 31) / 32;
                 uint32_t v[2][32];
-                tmem_ld32(acc, v[0]);
-                if constexpr (EPI == EPI_BF16) {
-                    // pairs of rows, packed; the next chunk on its way
-                    uint32_t p[CH][16];
+                if (first_row(0) < rows) tmem_ld32(tbase + first_row(0), v[0]);
+                // bf16: pairs of rows, packed; fp32: as they are
+                constexpr int PER = EPI == EPI_BF16 ? 16 : 32;
+                uint32_t p[CH][PER];
 #pragma unroll
-                    for (int i = 0; i < CH; ++i) {
-                        if (32 * i < rows) {
-                            tmem_ld_wait(v[i & 1]);
-                            if (i + 1 < CH && 32 * (i + 1) < rows) tmem_ld32(acc + 32 * (i + 1), v[(i + 1) & 1]);
+                for (int i = 0; i < CH; ++i) {
+                    if (first_row(i) < rows) {
+                        tmem_ld_wait(v[i & 1]);
+                        if (i + 1 < CH && first_row(i + 1) < rows) tmem_ld32(tbase + first_row(i + 1), v[(i + 1) & 1]);
+                        if (g.bias) {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                p[i][j] = pack_bf16x2(__uint_as_float(v[i & 1][2 * j]) + bias,
-                                                      __uint_as_float(v[i & 1][2 * j + 1]) + bias);
+                            for (int j = 0; j < 32; ++j)
+                                v[i & 1][j] = __float_as_uint(__uint_as_float(v[i & 1][j]) + bias);
+                        }
+#pragma unroll
+                        for (int j = 0; j < PER; ++j) {
+                            if constexpr (EPI == EPI_BF16)
+                                p[i][j] = pack_bf16x2(__uint_as_float(v[i & 1][2 * j]), __uint_as_float(v[i & 1][2 * j + 1]));
+                            else
+                                p[i][j] = v[i & 1][j];
                         }
                     }
-                    release();
-                    // even lanes store two columns of the pair's first row,
-                    // odd lanes of its second
-                    const uint32_t pick = lane & 1 ? 0x3276u : 0x5410u;
-                    const int64_t step = 2 * static_cast<int64_t>(g.n_out);
-                    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(g.out) +
-                                         (row0 + (lane & 1)) * g.n_out + col0 + (lane & ~1);
-                    int left = col0 + (lane & ~1) < g.n_out ? rows - (lane & 1) : 0;  // rows from this one on
+                }
+                release();
+                // bf16: even lanes store two columns of a pair's first row,
+                // odd lanes of its second.  fp32: a column a lane.
+                constexpr int COLS = EPI == EPI_BF16 ? 2 : 1, ES = EPI == EPI_BF16 ? 2 : 4;
+                const uint32_t pick = lane & 1 ? 0x3276u : 0x5410u;
+                const int sub = EPI == EPI_BF16 ? lane & 1 : 0, c = col0 + lane - sub;
+                const int64_t row_bytes = static_cast<int64_t>(g.n_out) * ES;
+                uint8_t *out = static_cast<uint8_t *>(g.out) + (row0 + first_row(0) + sub) * row_bytes + static_cast<int64_t>(c) * ES;
+                int left = c < g.n_out ? rows - first_row(0) - sub : 0;  // rows from `out` on
 #pragma unroll
-                    for (int i = 0; i < CH; ++i) {
-                        if (32 * i >= rows) break;
+                for (int i = 0; i < CH; ++i) {
+                    if (first_row(i) < rows) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const uint32_t o = __shfl_xor_sync(0xffffffffu, p[i][j], 1);
-                            if (left > 0) *reinterpret_cast<uint32_t *>(out) = __byte_perm(p[i][j], o, pick);
-                            out += step;
-                            left -= 2;
+                        for (int j = 0; j < PER; ++j) {
+                            uint32_t w = p[i][j];
+                            if constexpr (EPI == EPI_BF16) w = __byte_perm(w, __shfl_xor_sync(0xffffffffu, w, 1), pick);
+                            store_if(left > 0, out, w);
+                            out += COLS * row_bytes;
+                            left -= COLS;
                         }
-                    }
-                } else {
-                    float *out = static_cast<float *>(g.out) + row0 * g.n_out + col;
-                    int left = col < g.n_out ? rows : 0;
-#pragma unroll
-                    for (int i = 0; i < CH; ++i) {
-                        if (32 * i < rows) {
-                            tmem_ld_wait(v[i & 1]);
-                            if (i + 1 < CH && 32 * (i + 1) < rows) tmem_ld32(acc + 32 * (i + 1), v[(i + 1) & 1]);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                if (left > j) *out = __uint_as_float(v[i & 1][j]) + bias;
-                                out += g.n_out;
-                            }
+                        if (!kHalfAcc) {  // past the other half's chunk
+                            out += 32 * row_bytes;
                             left -= 32;
                         }
                     }
-                    release();
                 }
             }
         }
@@ -590,33 +613,33 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 }
 
-template <int EPI, bool BIG> cudaError_t launch(const Fp8GemmArgs &a, int num_sms, cudaStream_t s)
+template <int EPI, typename S> cudaError_t launch(const Fp8GemmArgs &a, int num_sms, cudaStream_t s)
 {
-    using S = Shape<BIG>;
     RowMaps tmA;
     CUtensorMap tmW, tmW3;
     constexpr bool kTwo = EPI == EPI_SWIGLU;
+    constexpr int TILE_N = kTwo ? WM : S::ACC * WM;
     for (int i = 0; i < 4; ++i)
         if (!make_tmap_u8(&tmA.box[i], a.a, a.k, a.rows, 1, 128u >> i)) return cudaErrorInvalidValue;
-    if (!make_tmap_u8(&tmW, a.w, a.k, a.n, a.E, kTwo ? WM : 2 * WM) ||
-        !make_tmap_u8(&tmW3, kTwo ? a.w3 : a.w, a.k, a.n, a.E, kTwo ? WM : 2 * WM))
+    if (!make_tmap_u8(&tmW, a.w, a.k, a.n, a.E, TILE_N) || !make_tmap_u8(&tmW3, kTwo ? a.w3 : a.w, a.k, a.n, a.E, TILE_N))
         return cudaErrorInvalidValue;
-    auto *kernel = ffn_gemm_mxfp8_kernel<EPI, BIG>;
-    cudaError_t err = ensure_smem_attr(reinterpret_cast<const void *>(kernel), static_cast<int>(smem_bytes<BIG>()));
+    auto *kernel = ffn_gemm_mxfp8_kernel<EPI, S>;
+    cudaError_t err = ensure_smem_attr(reinterpret_cast<const void *>(kernel), static_cast<int>(smem_bytes<S>()));
     if (err != cudaSuccess) return err;
-    const GemmArgs g = gemm_args(a, kTwo ? WM : 2 * WM);
+    const GemmArgs g = gemm_args(a, TILE_N);
     // every slice may end inside a tile
     const int64_t most = (a.rows / S::NMAX + min64(a.E, a.rows)) * g.n_tiles;
     if (most >= (static_cast<int64_t>(1) << 31)) return cudaErrorInvalidValue;
     const dim3 grid(static_cast<unsigned>(min64(most, num_sms)));
-    return launch_k(kernel, grid, dim3(THREADS), smem_bytes<BIG>(), s, tmA, tmW, tmW3, g);
+    return launch_k(kernel, grid, dim3(THREADS), smem_bytes<S>(), s, tmA, tmW, tmW3, g);
 }
 
-// Slices that average more rows than a small tile holds take the BIG one.
+// Slices that average more rows than the small tiles are good for take the
+// wide ones.
 template <int EPI> cudaError_t by_rows(const Fp8GemmArgs &a, int num_sms, cudaStream_t s)
 {
-    return a.rows > Shape<false>::NMAX * static_cast<int64_t>(a.E) ? launch<EPI, true>(a, num_sms, s)
-                                                                     : launch<EPI, false>(a, num_sms, s);
+    return a.rows > kFewRows * static_cast<int64_t>(a.E) ? launch<EPI, Wide>(a, num_sms, s)
+                                                          : launch<EPI, Few>(a, num_sms, s);
 }
 
 }  // namespace
@@ -626,9 +649,9 @@ cudaError_t launch_gemm_mxfp8(const Fp8GemmArgs &a, int num_sms, cudaStream_t s)
     if (a.rows == 0) return cudaSuccess;
     switch (a.epi) {
         case kFp8Swiglu: return by_rows<EPI_SWIGLU>(a, num_sms, s);
-        case kFp8Gelu: return launch<EPI_GELU, false>(a, num_sms, s);
+        case kFp8Gelu: return launch<EPI_GELU, Tall>(a, num_sms, s);
         case kFp8Bf16: return by_rows<EPI_BF16>(a, num_sms, s);
-        default: return launch<EPI_F32, false>(a, num_sms, s);
+        default: return launch<EPI_F32, Tall>(a, num_sms, s);
     }
 }
 
