@@ -85,7 +85,10 @@ template <int ACC_, int NMAX_, int BUFS_> struct Shape {
 using Wide = Shape<2, 240, 1>;
 using Tall = Shape<1, 240, 2>;
 using Few = Shape<2, 112, 2>;
-constexpr int kFewRows = 80;  // average rows of a slice up to which Few is taken
+// Average rows of a slice up to which Few is taken.  8 slices, n = 8192, k =
+// 4096: 64 rows 58 us and 63 (wide), 112 rows 79 and 65; slices of a random
+// routing spread around the average.
+constexpr int kFewRows = 80;
 
 struct RowMaps {
     CUtensorMap box[4];  // 128, 64, 32, 16 rows
@@ -642,6 +645,19 @@ template <int EPI> cudaError_t by_rows(const Fp8GemmArgs &a, int num_sms, cudaSt
                                                           : launch<EPI, Few>(a, num_sms, s);
 }
 
+// Few waves of tiles: a wave of tall tiles takes about 0.59 of one of wide
+// tiles (735 against 1230 cycles a k-block, by the bytes of shared memory),
+// so twice as many of them can fill the SMs better.  8 x 600 rows, n = k =
+// 2048: 28 us tall, 31 wide; 4096 rows of one expert, n = k = 4096: 63 and 56.
+bool tall_is_better(const Fp8GemmArgs &a, int num_sms)
+{
+    const int64_t each = (a.rows + a.E - 1) / a.E;
+    if (each <= kFewRows) return false;
+    const int64_t row_tiles = (each + Wide::NMAX - 1) / Wide::NMAX * a.E;
+    auto waves = [&](int64_t tile_n) { return (row_tiles * ((a.n + tile_n - 1) / tile_n) + num_sms - 1) / num_sms; };
+    return 100 * waves(2 * WM) > 59 * waves(WM);
+}
+
 }  // namespace
 
 cudaError_t launch_gemm_mxfp8(const Fp8GemmArgs &a, int num_sms, cudaStream_t s)
@@ -650,7 +666,7 @@ cudaError_t launch_gemm_mxfp8(const Fp8GemmArgs &a, int num_sms, cudaStream_t s)
     switch (a.epi) {
         case kFp8Swiglu: return by_rows<EPI_SWIGLU>(a, num_sms, s);
         case kFp8Gelu: return launch<EPI_GELU, Tall>(a, num_sms, s);
-        case kFp8Bf16: return by_rows<EPI_BF16>(a, num_sms, s);
+        case kFp8Bf16: return tall_is_better(a, num_sms) ? launch<EPI_BF16, Tall>(a, num_sms, s) : by_rows<EPI_BF16>(a, num_sms, s);
         default: return launch<EPI_F32, Tall>(a, num_sms, s);
     }
 }
