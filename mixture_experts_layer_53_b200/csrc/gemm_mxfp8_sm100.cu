@@ -21,15 +21,17 @@
 // run at the same time share an expert's weight tile through L2.
 //
 // Where arithmetic bounds it, it is shared memory that does: an MMA of N rows
-// takes N / 2 cycles and reads 4 KB of weights and 32 N bytes of rows.  Three
-// shapes share the 512 TMEM columns:
-//   two accumulators of 240 rows: fewest bytes from L2 and shared memory per
-//     product.  Its epilogue holds the tile in registers, so that the next
-//     tile's MMAs wait for the TMEM reads only.
-//   one accumulator of 240 rows, twice: for epilogues that cannot hold two (fp32
-//     results, GELU); they overlap the next tile's MMAs.
-//   two of 112 rows, twice: slices of few rows, bound by reading weights.  Four
-//     stages instead of three, and an epilogue that overlaps.
+// takes N / 2 cycles and reads 4 KB of weights and 32 N bytes of rows, and
+// the next k-blocks are written meanwhile.  The shapes share 512 TMEM columns
+// and 186 KB of stages:
+//   Wide      two accumulators of 240 rows: fewest bytes from L2 and shared
+//             memory per product.  The next tile's MMAs wait until its
+//             epilogue has read it.
+//   Tall      one accumulator of 240 rows, twice: the epilogue overlaps, and
+//             there are twice as many tiles.
+//   Few       two of 112 rows, twice, for slices of few rows: bound by reading
+//             weights, with four stages instead of three.
+//   Tiny, TinyTall  two or one of 32 rows, with five or nine stages.
 //
 // Warp roles (384 threads, one CTA per SM, persistent):
 //   warp 0      TMA producer: per k-block of 128 values W (16 KB for each
@@ -75,7 +77,7 @@ template <int ACC_, int NMAX_, int BUFS_> struct Shape {
     static constexpr int ATOMS = NMAX > 128 ? 2 : 1;  // 128-row scale tiles of the rows
     static constexpr int W_BYTES = ACC * WM * BK;
     static constexpr int STAGE = W_BYTES + NMAX * BK;
-    static constexpr int STAGES = STAGE > 48 * 1024 ? 3 : 4;
+    static constexpr int STAGES = 186 * 1024 / STAGE;
     static constexpr uint32_t SCALE_COL = ACC * BUFS * NMAX;
     static constexpr uint32_t SLOT_COLS = 4 * ACC + 4 * ATOMS;  // of the weights, of the rows; two slots
     static_assert(SCALE_COL + 2 * SLOT_COLS <= TMEM_COLS, "TMEM columns");
@@ -85,10 +87,13 @@ template <int ACC_, int NMAX_, int BUFS_> struct Shape {
 using Wide = Shape<2, 240, 1>;
 using Tall = Shape<1, 240, 2>;
 using Few = Shape<2, 112, 2>;
-// Average rows of a slice up to which Few is taken.  8 slices, n = 8192, k =
-// 4096: 64 rows 58 us and 63 (wide), 112 rows 79 and 65; slices of a random
-// routing spread around the average.
-constexpr int kFewRows = 80;
+using Tiny = Shape<2, 32, 2>;
+using TinyTall = Shape<1, 32, 2>;
+// Average rows of a slice up to which Tiny and Few are taken; slices of a
+// random routing spread around the average.  n = 4096, k = 14336, 4 rows:
+// 75.4 us Tiny, 77.2 Few; n = k = 4096, 32 rows: 46 Tiny, 28 Few; n = 8192, k =
+// 4096 and 64 rows: 58 Few, 63 Wide, 112 rows: 79 Few, 65 Wide (8 slices).
+constexpr int kTinyRows = 16, kFewRows = 80;
 
 struct RowMaps {
     CUtensorMap box[4];  // 128, 64, 32, 16 rows
@@ -114,7 +119,8 @@ template <typename S> struct Ctl {
 };
 
 template <typename S> constexpr size_t smem_bytes() { return 1024 + S::STAGES * S::STAGE + sizeof(Ctl<S>); }
-static_assert(smem_bytes<Wide>() <= 232448 && smem_bytes<Tall>() <= 232448 && smem_bytes<Few>() <= 232448,
+static_assert(smem_bytes<Wide>() <= 232448 && smem_bytes<Tall>() <= 232448 && smem_bytes<Few>() <= 232448 &&
+                  smem_bytes<Tiny>() <= 232448 && smem_bytes<TinyTall>() <= 232448,
               "shared memory per CTA");
 
 // Instruction descriptor of kind::mxf8f6f4: A and B e4m3 (0) and K-major, N >> 3
@@ -192,7 +198,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr bool kHidden = EPI == EPI_SWIGLU || EPI == EPI_GELU;
     // the epilogue's halves: an accumulator each, or every other 32 rows
     constexpr bool kHalfAcc = S::ACC == 2 && EPI != EPI_SWIGLU;
-    static_assert(EPI == EPI_BF16 || S::ACC == (EPI == EPI_SWIGLU ? 2 : 1), "a tile fits the epilogue's registers");
+    static_assert(EPI != EPI_SWIGLU || S::ACC == 2, "gate and up");
+    static_assert(EPI != EPI_GELU || S::ACC == 1, "a tile fits the epilogue's registers");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *tiles = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                  ~static_cast<uintptr_t>(1023));
@@ -554,55 +561,60 @@ __global__ void __launch_bounds__(THREADS, 1)
                     release();
                     continue;
                 }
-                uint32_t v[2][32];
-                if (first_row(0) < rows) tmem_ld32(tbase + first_row(0), v[0]);
-                // bf16: pairs of rows, packed; fp32: as they are
-                constexpr int PER = EPI == EPI_BF16 ? 16 : 32;
-                uint32_t p[CH][PER];
-#pragma unroll
-                for (int i = 0; i < CH; ++i) {
-                    if (first_row(i) < rows) {
-                        tmem_ld_wait(v[i & 1]);
-                        if (i + 1 < CH && first_row(i + 1) < rows) tmem_ld32(tbase + first_row(i + 1), v[(i + 1) & 1]);
-                        if (g.bias) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                v[i & 1][j] = __float_as_uint(__uint_as_float(v[i & 1][j]) + bias);
-                        }
-#pragma unroll
-                        for (int j = 0; j < PER; ++j) {
-                            if constexpr (EPI == EPI_BF16)
-                                p[i][j] = pack_bf16x2(__uint_as_float(v[i & 1][2 * j]), __uint_as_float(v[i & 1][2 * j + 1]));
-                            else
-                                p[i][j] = v[i & 1][j];
-                        }
-                    }
-                }
-                release();
-                // bf16: even lanes store two columns of a pair's first row,
-                // odd lanes of its second.  fp32: a column a lane.
-                constexpr int COLS = EPI == EPI_BF16 ? 2 : 1, ES = EPI == EPI_BF16 ? 2 : 4;
+                // bf16: pairs of rows, packed; even lanes store two columns of
+                // a pair's first row, odd lanes of its second.  fp32: a
+                // column a lane.
+                constexpr bool kBf16 = EPI == EPI_BF16;
+                constexpr int PER = kBf16 ? 16 : 32, ROWS = kBf16 ? 2 : 1, ES = kBf16 ? 2 : 4;
                 const uint32_t pick = lane & 1 ? 0x3276u : 0x5410u;
-                const int sub = EPI == EPI_BF16 ? lane & 1 : 0, c = col0 + lane - sub;
+                const int sub = kBf16 ? lane & 1 : 0, c = col0 + lane - sub;
                 const int64_t row_bytes = static_cast<int64_t>(g.n_out) * ES;
                 uint8_t *out = static_cast<uint8_t *>(g.out) + (row0 + first_row(0) + sub) * row_bytes + static_cast<int64_t>(c) * ES;
                 int left = c < g.n_out ? rows - first_row(0) - sub : 0;  // rows from `out` on
+                auto store = [&](const uint32_t (&p)[PER]) {
+#pragma unroll
+                    for (int j = 0; j < PER; ++j) {
+                        uint32_t w = p[j];
+                        if constexpr (kBf16) w = __byte_perm(w, __shfl_xor_sync(0xffffffffu, w, 1), pick);
+                        store_if(left > 0, out, w);
+                        out += ROWS * row_bytes;
+                        left -= ROWS;
+                    }
+                    if (!kHalfAcc) {  // past the other half's chunk
+                        out += 32 * row_bytes;
+                        left -= 32;
+                    }
+                };
+                // The tile is held in registers where they suffice, and
+                // TMEM released before the first store.
+                constexpr bool kHold = CH * PER <= 128;
+                uint32_t v[2][32], p[kHold ? CH : 1][PER];
+                if (first_row(0) < rows) tmem_ld32(tbase + first_row(0), v[0]);
 #pragma unroll
                 for (int i = 0; i < CH; ++i) {
                     if (first_row(i) < rows) {
+                        uint32_t(&x)[32] = v[i & 1];
+                        tmem_ld_wait(x);
+                        if (i + 1 < CH && first_row(i + 1) < rows) tmem_ld32(tbase + first_row(i + 1), v[(i + 1) & 1]);
+                        else if (!kHold) release();
+                        if (g.bias) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) + bias);
+                        }
+                        uint32_t(&q)[PER] = p[kHold ? i : 0];
 #pragma unroll
                         for (int j = 0; j < PER; ++j) {
-                            uint32_t w = p[i][j];
-                            if constexpr (EPI == EPI_BF16) w = __byte_perm(w, __shfl_xor_sync(0xffffffffu, w, 1), pick);
-                            store_if(left > 0, out, w);
-                            out += COLS * row_bytes;
-                            left -= COLS;
+                            if constexpr (kBf16) q[j] = pack_bf16x2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]));
+                            else q[j] = x[j];
                         }
-                        if (!kHalfAcc) {  // past the other half's chunk
-                            out += 32 * row_bytes;
-                            left -= 32;
-                        }
+                        if (!kHold) store(q);
                     }
+                }
+                if (kHold || first_row(0) >= rows) release();
+                if constexpr (kHold) {
+#pragma unroll
+                    for (int i = 0; i < CH; ++i)
+                        if (first_row(i) < rows) store(p[i]);
                 }
             }
         }
@@ -637,25 +649,35 @@ template <int EPI, typename S> cudaError_t launch(const Fp8GemmArgs &a, int num_
     return launch_k(kernel, grid, dim3(THREADS), smem_bytes<S>(), s, tmA, tmW, tmW3, g);
 }
 
-// Slices that average more rows than the small tiles are good for take the
-// wide ones.
-template <int EPI> cudaError_t by_rows(const Fp8GemmArgs &a, int num_sms, cudaStream_t s)
-{
-    return a.rows > kFewRows * static_cast<int64_t>(a.E) ? launch<EPI, Wide>(a, num_sms, s)
-                                                          : launch<EPI, Few>(a, num_sms, s);
-}
-
-// Few waves of tiles: a wave of tall tiles takes about 0.59 of one of wide
-// tiles (735 against 1230 cycles a k-block, by the bytes of shared memory),
-// so twice as many of them can fill the SMs better.  8 x 600 rows, n = k =
-// 2048: 28 us tall, 31 wide; 4096 rows of one expert, n = k = 4096: 63 and 56.
-bool tall_is_better(const Fp8GemmArgs &a, int num_sms)
+// Which shape: by the average rows of a slice, and where few waves of tiles
+// fill the SMs, by how many there are.
+enum { WIDE, TALL, FEW, TINY, TINY_TALL };
+int shape_of(const Fp8GemmArgs &a, int num_sms)
 {
     const int64_t each = (a.rows + a.E - 1) / a.E;
-    if (each <= kFewRows) return false;
-    const int64_t row_tiles = (each + Wide::NMAX - 1) / Wide::NMAX * a.E;
-    auto waves = [&](int64_t tile_n) { return (row_tiles * ((a.n + tile_n - 1) / tile_n) + num_sms - 1) / num_sms; };
-    return 100 * waves(2 * WM) > 59 * waves(WM);
+    auto tiles = [&](int64_t slices, int64_t tile_n) { return slices * ((a.n + tile_n - 1) / tile_n); };
+    // fewer weight tiles than half the SMs: smaller ones keep more SMs reading
+    // (one row, n = k = 4096: 25 us by 16 tiles, 18 by 32; 128 tiles: equal)
+    if (each <= kTinyRows) return tiles(min64(a.rows, a.E), WM) <= num_sms ? TINY_TALL : TINY;
+    if (each <= kFewRows) return FEW;
+    // A wave of tall tiles takes about 0.59 of one of wide tiles (735 against
+    // 1230 cycles a k-block, by the bytes of shared memory), so twice as many
+    // of them can fill the SMs better.  8 x 600 rows, n = k = 2048: 28 us tall,
+    // 31 wide; 4096 rows of one expert, n = k = 4096: 63 and 56.
+    const int64_t slices = (each + Wide::NMAX - 1) / Wide::NMAX * a.E;
+    auto waves = [&](int64_t tile_n) { return (tiles(slices, tile_n) + num_sms - 1) / num_sms; };
+    return 100 * waves(2 * WM) > 59 * waves(WM) ? TALL : WIDE;
+}
+
+template <int EPI> cudaError_t launch_rows(const Fp8GemmArgs &a, int num_sms, cudaStream_t s)
+{
+    switch (shape_of(a, num_sms)) {
+        case WIDE: return launch<EPI, Wide>(a, num_sms, s);
+        case TALL: return launch<EPI, Tall>(a, num_sms, s);
+        case FEW: return launch<EPI, Few>(a, num_sms, s);
+        case TINY: return launch<EPI, Tiny>(a, num_sms, s);
+        default: return launch<EPI, TinyTall>(a, num_sms, s);
+    }
 }
 
 }  // namespace
@@ -663,11 +685,16 @@ bool tall_is_better(const Fp8GemmArgs &a, int num_sms)
 cudaError_t launch_gemm_mxfp8(const Fp8GemmArgs &a, int num_sms, cudaStream_t s)
 {
     if (a.rows == 0) return cudaSuccess;
+    const int64_t each = (a.rows + a.E - 1) / a.E;
     switch (a.epi) {
-        case kFp8Swiglu: return by_rows<EPI_SWIGLU>(a, num_sms, s);
-        case kFp8Gelu: return launch<EPI_GELU, Tall>(a, num_sms, s);
-        case kFp8Bf16: return tall_is_better(a, num_sms) ? launch<EPI_BF16, Tall>(a, num_sms, s) : by_rows<EPI_BF16>(a, num_sms, s);
-        default: return launch<EPI_F32, Tall>(a, num_sms, s);
+        case kFp8Swiglu:  // always two accumulators, gate and up
+            return each <= kTinyRows  ? launch<EPI_SWIGLU, Tiny>(a, num_sms, s)
+                   : each <= kFewRows ? launch<EPI_SWIGLU, Few>(a, num_sms, s)
+                                      : launch<EPI_SWIGLU, Wide>(a, num_sms, s);
+        case kFp8Gelu:  // always one: a thread holds its values
+            return each <= kTinyRows ? launch<EPI_GELU, TinyTall>(a, num_sms, s) : launch<EPI_GELU, Tall>(a, num_sms, s);
+        case kFp8Bf16: return launch_rows<EPI_BF16>(a, num_sms, s);
+        default: return launch_rows<EPI_F32>(a, num_sms, s);
     }
 }
 

@@ -145,7 +145,11 @@ PRODUCTS = {
     "long_k": ([2, 0, 40], 144, 4112),
     "one_expert": ([700], 528, 640),
     "many_experts": ([i % 5 for i in range(256)], 128, 272),
-    "pairs": ([256, 255, 257, 1000], 1040, 720),
+    "long_slices": ([256, 255, 257, 1000], 1040, 720),
+    "wide": ([500, 241, 479, 700], 2560, 400),
+    "tiny": ([2, 0, 5, 1, 1, 16, 17, 33], 2576, 272),
+    "tiny_but_one": ([100] + [0] * 14 + [1], 528, 400),
+    "few": ([16, 112, 113, 0, 47], 272, 656),
     "many_tiles": ([300, 4, 500, 0, 900, 129, 10, 250], 1552, 384),
 }
 
