@@ -31,7 +31,10 @@
 //             there are twice as many tiles.
 //   Few       two of 112 rows, twice, for slices of few rows: bound by reading
 //             weights, with four stages instead of three.
-//   Tiny, TinyTall  two or one of 32 rows, with five or nine stages.
+//   Tiny, TinyTall  two or one of 32 rows, with five or nine stages.  With
+//             tiles for a part of the SMs only, a cluster of two to eight
+//             CTAs shares a tile's k-blocks; their accumulators are added
+//             in rank order through distributed shared memory.
 //
 // Warp roles (384 threads, one CTA per SM, persistent):
 //   warp 0      TMA producer: per k-block of 128 values W (16 KB for each
@@ -171,6 +174,19 @@ __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_gr
 // Until all but this thread's last N groups of copies have landed.
 template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+__device__ __forceinline__ uint32_t cluster_nctas()
+{
+    uint32_t n;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+    return n;
+}
+__device__ __forceinline__ float load_cluster(uint32_t cluster_addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr));
+    return v;
+}
+
 // A predicated 4-byte store (a branch around a plain one costs the unrolled
 // epilogues up to a third of their time).
 __device__ __forceinline__ void store_if(bool p, void *dst, uint32_t v)
@@ -190,7 +206,15 @@ __device__ __forceinline__ uint32_t transpose4(uint32_t w, int lane)
     return __byte_perm(w, z, lane & 2 ? 0x3276u : 0x5410u);
 }
 
-template <int EPI, typename S>
+// Tiles at most: every slice may end inside one.
+template <typename S> int64_t most_tiles(const Fp8GemmArgs &a, int64_t n_tiles)
+{
+    return (a.rows / S::NMAX + min64(a.E, a.rows)) * n_tiles;
+}
+
+// SPLIT: a cluster of CTAs per tile, each with its share of the k-blocks;
+// one tile per cluster (the grid has room for all).
+template <int EPI, typename S, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1)
     ffn_gemm_mxfp8_kernel(const __grid_constant__ RowMaps tmA, const __grid_constant__ CUtensorMap tmW,
                           const __grid_constant__ CUtensorMap tmW3, const GemmArgs g)
@@ -235,6 +259,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         tmem_relinquish();
     }
     // nothing above touches memory that an earlier kernel writes
+    const int ranks = SPLIT ? static_cast<int>(cluster_nctas()) : 1, rank = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
     pdl_enter();
     tc_fence_before();
     load_slices<S::NMAX>(&ctl->slices, g);
@@ -243,7 +268,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const Slices *sl = &ctl->slices;
     const uint32_t tmem_base = ctl->tmem_base;
     const int total = sl->mt[g.E] * g.n_tiles;
+    const int first = static_cast<int>(blockIdx.x) / ranks, step = static_cast<int>(gridDim.x) / ranks;
     const int num_kb = (g.K + BK - 1) / BK;
+    const int kb_lo = SPLIT ? rank * num_kb / ranks : 0, kb_hi = SPLIT ? (rank + 1) * num_kb / ranks : num_kb;
     constexpr int TILE_N = EPI == EPI_SWIGLU ? WM : S::ACC * WM;  // result columns of a tile
     // A slice's rows in tiles of equal size (a multiple of 16): the tiles of a
     // wave then take equally long.
@@ -263,11 +290,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             int stage = 0;
             uint32_t phase = 0, armed = 0, armed_parity = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+            for (int t = first; t < total && ok; t += step) {
                 const Tile ti = decode_tile(t, sl, g.E, g.n_tiles);
                 const Rows tr = rows_of(ti);
                 const int row0 = tr.first, n0 = ti.n_tile * TILE_N, n = (tr.count + 15) & ~15;
-                for (int kb = 0; kb < num_kb; ++kb) {
+                for (int kb = kb_lo; kb < kb_hi; ++kb) {
                     if (!mbar_wait(&ctl->empty[stage], phase ^ 1u, abort_flag, g.status)) {
                         ok = false;
                         break;
@@ -305,14 +332,14 @@ __global__ void __launch_bounds__(THREADS, 1)
             int stage = 0, buf = 0;
             uint32_t phase = 0, tphase = 0, group = 0;
             bool ok = true, issued = false;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+            for (int t = first; t < total && ok; t += step) {
                 const Tile ti = decode_tile(t, sl, g.E, g.n_tiles);
                 const int n = (rows_of(ti).count + 15) & ~15;
                 const bool both = S::ACC == 2 && (EPI == EPI_SWIGLU || ti.n_tile * TILE_N + WM < g.n_out);
                 if (!mbar_wait(&ctl->tempty[buf], tphase ^ 1u, abort_flag, g.status)) break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + static_cast<uint32_t>(buf * S::ACC * S::NMAX);
-                for (int kb0 = 0; kb0 < num_kb && ok; kb0 += GROUP) {
+                for (int kb0 = kb_lo; kb0 < kb_hi && ok; kb0 += GROUP) {
                     // The group's scales are there, and the MMAs of the
                     // group before the last, which read the same TMEM
                     // columns, are done.
@@ -331,7 +358,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     copy_scales(sr, desc_scales(src + 1024));
                     if (S::ATOMS == 2) copy_scales(sr + 4u, desc_scales(src + 1536));
                     issued = true;
-                    const int kbs = min(GROUP, num_kb - kb0);
+                    const int kbs = min(GROUP, kb_hi - kb0);
                     for (int j = 0; j < kbs; ++j) {
                         if (!mbar_wait(&ctl->full[stage], phase, abort_flag, g.status)) {
                             ok = false;
@@ -339,7 +366,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                         tc_fence_after();
                         const uint32_t w_addr = smem_u32(tiles + stage * S::STAGE), a_addr = w_addr + S::W_BYTES;
-                        const uint32_t idesc = idesc_mxf8(n, j), add = (kb0 | j) != 0 ? 1u : 0u;
+                        const uint32_t idesc = idesc_mxf8(n, j), add = kb0 + j != kb_lo ? 1u : 0u;
 #pragma unroll
                         for (int kk = 0; kk < BK / 32; ++kk)
                             umma_mxf8(d, desc_sw128(w_addr + kk * 32), desc_sw128(a_addr + kk * 32), idesc, sw, sr,
@@ -382,7 +409,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             // weights.  1 where there is none.
             Tile ti{};
             Rows tr{};
-            int t_ahead = blockIdx.x, kb_ahead = 0, decoded = -1;
+            int t_ahead = first, kb_ahead = kb_lo, decoded = -1;
             auto fetch = [&](float (&to)[4 * GROUP + 1][32]) {
                 if (t_ahead < total) {
                     if (decoded != t_ahead) {
@@ -397,7 +424,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                         for (int j = 0; j < GROUP; ++j) {
                             float *dst = &to[i * GROUP + j][lane];
-                            if (r < tr.count && kb_ahead + j < num_kb) copy_ahead(dst, p + static_cast<int64_t>(j) * g.rows);
+                            if (r < tr.count && kb_ahead + j < kb_hi) copy_ahead(dst, p + static_cast<int64_t>(j) * g.rows);
                             else *dst = 1.0f;
                         }
                     }
@@ -406,13 +433,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const float *p = (EPI == EPI_SWIGLU && h ? g.w3_scales : g.w_scales) +
                                      (static_cast<int64_t>(ti.e) * nblocks + nb) * num_kb;
                     float *dst = &to[4 * GROUP][lane];
-                    if (atom == 0 && lane < 8 && j < num_kb) copy_ahead(dst, p + j);
+                    if (atom == 0 && lane < 8 && j < kb_hi) copy_ahead(dst, p + j);
                     else *dst = 1.0f;
                 }
                 copy_commit();
-                if ((kb_ahead += GROUP) >= num_kb) {
-                    kb_ahead = 0;
-                    t_ahead += gridDim.x;
+                if ((kb_ahead += GROUP) >= kb_hi) {
+                    kb_ahead = kb_lo;
+                    t_ahead += step;
                 }
             };
             // exponent codes; a scale that is no power of two (zero,
@@ -425,8 +452,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int i = 0; i + 1 < AHEAD; ++i) fetch(ctl->ahead[atom][i]);
             uint32_t group = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-                for (int kb0 = 0; kb0 < num_kb; kb0 += GROUP, ++group) {
+            for (int t = first; t < total && ok; t += step) {
+                for (int kb0 = kb_lo; kb0 < kb_hi; kb0 += GROUP, ++group) {
                     fetch(ctl->ahead[atom][(group + AHEAD - 1) % AHEAD]);
                     copy_wait<AHEAD - 1>();
                     const float(&a)[4 * GROUP + 1][32] = ctl->ahead[atom][group % AHEAD];
@@ -461,13 +488,36 @@ __global__ void __launch_bounds__(THREADS, 1)
             copy_wait<0>();  // none of this thread's copies is left behind
             if (odd_scale) set_status(g.status, kDevBadArgument);
         }
+        if constexpr (SPLIT) {
+            __syncwarp();
+            cluster_sync();  // the other warps' comes with the exchange of accumulators
+        }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SUM_REGS));
         // ---------------------------------------------------- epilogue
         const int quarter = warp & 3, half = (warp - FIRST_SUM_WARP) >> 2;
         int buf = 0;
         uint32_t tphase = 0, xphase = 0;
-        for (int t = blockIdx.x; t < total; t += gridDim.x) {
+        bool met = false;
+        // SPLIT: the others leave this thread's accumulator values of one
+        // chunk of rows (accumulator i) in shared memory; after the cluster
+        // has met, rank 0 adds them.
+        float *part = reinterpret_cast<float *>(tiles) + quarter * 32 + lane;
+        auto leave = [&](const uint32_t (&v)[32], int i, int rows) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (j < rows) part[(32 * i + j) * WM] = __uint_as_float(v[j]);
+        };
+        auto gather = [&](uint32_t (&v)[32], int i, int rows) {
+            for (int r = 1; r < ranks; ++r) {
+                const uint32_t from = mapa_shared(smem_u32(part + 32 * i * WM), static_cast<uint32_t>(r));
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (j < rows)
+                        v[j] = __float_as_uint(__uint_as_float(v[j]) + load_cluster(from + static_cast<uint32_t>(j * WM * 4)));
+            }
+        };
+        for (int t = first; t < total; t += step) {
             const Tile ti = decode_tile(t, sl, g.E, g.n_tiles);
             const Rows tr = rows_of(ti);
             const int rows = tr.count;
@@ -514,6 +564,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                         tmem_ld32(tbase + r0, v);
                         tmem_ld_wait(v);
                     }
+                    if constexpr (SPLIT) {  // one chunk, of the first half
+                        if (rank != 0) {
+                            leave(v, 0, rows);
+                            if (EPI == EPI_SWIGLU) leave(up, 1, rows);
+                        }
+                        cluster_sync();
+                        met = true;
+                        if (rank != 0) break;
+                        gather(v, 0, rows);
+                        if (EPI == EPI_SWIGLU) gather(up, 1, rows);
+                    }
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
                         if constexpr (EPI == EPI_SWIGLU)
@@ -525,6 +586,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
                 release();
+                if (SPLIT && rank != 0) break;
                 // over the four lane quarters; two sets of values by phase: a
                 // warp that is a tile ahead writes the other set, and it
                 // cannot be two ahead
@@ -595,6 +657,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (first_row(i) < rows) {
                         uint32_t(&x)[32] = v[i & 1];
                         tmem_ld_wait(x);
+                        if constexpr (SPLIT) {  // one chunk, of the first half
+                            if (rank != 0) leave(x, 0, rows);
+                            cluster_sync();
+                            met = true;
+                            if (rank != 0) break;
+                            gather(x, 0, rows);
+                        }
                         if (i + 1 < CH && first_row(i + 1) < rows) tmem_ld32(tbase + first_row(i + 1), v[(i + 1) & 1]);
                         else if (!kHold) release();
                         if (g.bias) {
@@ -610,6 +679,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (!kHold) store(q);
                     }
                 }
+                if (SPLIT && rank != 0) break;
                 if (kHold || first_row(0) >= rows) release();
                 if constexpr (kHold) {
 #pragma unroll
@@ -618,18 +688,26 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
         }
+        if (SPLIT && !met) {
+            __syncwarp();
+            cluster_sync();
+        }
     }
 
     tc_fence_before();
     __syncthreads();
+    // nobody's shared memory goes while rank 0 reads it
+    if constexpr (SPLIT) cluster_sync();
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem_base, TMEM_COLS);
     }
 }
 
-template <int EPI, typename S> cudaError_t launch(const Fp8GemmArgs &a, int num_sms, cudaStream_t s)
+template <int EPI, typename S, bool SPLIT = false>
+cudaError_t launch(const Fp8GemmArgs &a, int num_sms, cudaStream_t s, int ranks = 1)
 {
+    static_assert(!SPLIT || S::NMAX <= 32, "one chunk of rows is exchanged");
     RowMaps tmA;
     CUtensorMap tmW, tmW3;
     constexpr bool kTwo = EPI == EPI_SWIGLU;
@@ -638,15 +716,26 @@ template <int EPI, typename S> cudaError_t launch(const Fp8GemmArgs &a, int num_
         if (!make_tmap_u8(&tmA.box[i], a.a, a.k, a.rows, 1, 128u >> i)) return cudaErrorInvalidValue;
     if (!make_tmap_u8(&tmW, a.w, a.k, a.n, a.E, TILE_N) || !make_tmap_u8(&tmW3, kTwo ? a.w3 : a.w, a.k, a.n, a.E, TILE_N))
         return cudaErrorInvalidValue;
-    auto *kernel = ffn_gemm_mxfp8_kernel<EPI, S>;
+    auto *kernel = ffn_gemm_mxfp8_kernel<EPI, S, SPLIT>;
     cudaError_t err = ensure_smem_attr(reinterpret_cast<const void *>(kernel), static_cast<int>(smem_bytes<S>()));
     if (err != cudaSuccess) return err;
     const GemmArgs g = gemm_args(a, TILE_N);
-    // every slice may end inside a tile
-    const int64_t most = (a.rows / S::NMAX + min64(a.E, a.rows)) * g.n_tiles;
-    if (most >= (static_cast<int64_t>(1) << 31)) return cudaErrorInvalidValue;
-    const dim3 grid(static_cast<unsigned>(min64(most, num_sms)));
-    return launch_k(kernel, grid, dim3(THREADS), smem_bytes<S>(), s, tmA, tmW, tmW3, g);
+    const int64_t most = most_tiles<S>(a, g.n_tiles);
+    if (most * ranks >= (static_cast<int64_t>(1) << 31)) return cudaErrorInvalidValue;
+    const dim3 grid(static_cast<unsigned>(SPLIT ? most * ranks : min64(most, num_sms)));
+    return launch_clusters(kernel, grid, dim3(THREADS), ranks, smem_bytes<S>(), s, tmA, tmW, tmW3, g);
+}
+
+// The small shapes, with a tile's k-blocks split where all tiles leave at
+// least half of the SMs idle and every part keeps two groups of k-blocks.
+template <int EPI, typename S> cudaError_t launch_split(const Fp8GemmArgs &a, int num_sms, cudaStream_t s)
+{
+    constexpr int TILE_N = EPI == EPI_SWIGLU ? WM : S::ACC * WM;
+    const int64_t most = most_tiles<S>(a, (a.n + TILE_N - 1) / TILE_N);
+    const int num_kb = (a.k + BK - 1) / BK;
+    for (int ranks = 8; ranks > 1; ranks /= 2)
+        if (most * ranks <= num_sms && num_kb >= 2 * GROUP * ranks) return launch<EPI, S, true>(a, num_sms, s, ranks);
+    return launch<EPI, S>(a, num_sms, s);
 }
 
 // Which shape: by the average rows of a slice, and where few waves of tiles
@@ -675,8 +764,8 @@ template <int EPI> cudaError_t launch_rows(const Fp8GemmArgs &a, int num_sms, cu
         case WIDE: return launch<EPI, Wide>(a, num_sms, s);
         case TALL: return launch<EPI, Tall>(a, num_sms, s);
         case FEW: return launch<EPI, Few>(a, num_sms, s);
-        case TINY: return launch<EPI, Tiny>(a, num_sms, s);
-        default: return launch<EPI, TinyTall>(a, num_sms, s);
+        case TINY: return launch<EPI, Tiny>(a, num_sms, s);  // more tiles than SMs
+        default: return launch_split<EPI, TinyTall>(a, num_sms, s);
     }
 }
 
@@ -688,11 +777,11 @@ cudaError_t launch_gemm_mxfp8(const Fp8GemmArgs &a, int num_sms, cudaStream_t s)
     const int64_t each = (a.rows + a.E - 1) / a.E;
     switch (a.epi) {
         case kFp8Swiglu:  // always two accumulators, gate and up
-            return each <= kTinyRows  ? launch<EPI_SWIGLU, Tiny>(a, num_sms, s)
+            return each <= kTinyRows  ? launch_split<EPI_SWIGLU, Tiny>(a, num_sms, s)
                    : each <= kFewRows ? launch<EPI_SWIGLU, Few>(a, num_sms, s)
                                       : launch<EPI_SWIGLU, Wide>(a, num_sms, s);
         case kFp8Gelu:  // always one: a thread holds its values
-            return each <= kTinyRows ? launch<EPI_GELU, TinyTall>(a, num_sms, s) : launch<EPI_GELU, Tall>(a, num_sms, s);
+            return each <= kTinyRows ? launch_split<EPI_GELU, TinyTall>(a, num_sms, s) : launch<EPI_GELU, Tall>(a, num_sms, s);
         case kFp8Bf16: return launch_rows<EPI_BF16>(a, num_sms, s);
         default: return launch_rows<EPI_F32>(a, num_sms, s);
     }
