@@ -462,8 +462,8 @@ MOE_API moe_status moe_permute_rows(int32_t dtype, const void *src, const int32_
  * Layouts, row-major and contiguous:
  *   activations  q [rows, cols] e4m3,    scales [ceil(cols/128), rows] f32
  *   weights      q [E, rows, cols] e4m3, scales [E, ceil(rows/128), ceil(cols/128)] f32
- * Limits: rows of activations < 2^31; widths multiples of 16 (else
- * MOE_ERR_UNSUPPORTED); every pointer but offsets 16-byte aligned.
+ * Limits: rows of activations < 2^31; widths multiples of 16, at most 2^30
+ * (else MOE_ERR_UNSUPPORTED); every pointer but offsets 16-byte aligned.
  */
 
 /* Quantises activations x [rows, cols] (dtype MOE_F32 or MOE_BF16). */
@@ -485,7 +485,10 @@ MOE_API moe_status moe_quantize_weights(int32_t dtype, const void *W, int32_t E,
  * its slice"): for the rows r = offsets[e] .. offsets[e+1]-1 of a
  *   out[r, c] = sum_j a[r, j] w[e, c, j],  a [rows, k], w [E, n, k] quantised
  * as above, out [rows, n] in out_dtype (MOE_F32 or MOE_BF16).  Products and
- * sums in fp32, rounded once at the end.  offsets [E+1] is read on the device
+ * sums in fp32, rounded once at the end (the tensor core's sums drop bits
+ * below a partial sum's last one: 8e-6 of the result for 14336 terms of one
+ * sign, 1e-6 for terms of either; any_scales = 1, which sums blocks of 128
+ * outside it, 1.6e-7).  offsets [E+1] is read on the device
  * and held inside 0 .. rows; rows outside every slice are left as they were.
  * E <= 256.  dev_status (may be NULL): MOE_ERR_TIMEOUT, MOE_ERR_INVALID_ARG
  * (scales, above).  No workspace.

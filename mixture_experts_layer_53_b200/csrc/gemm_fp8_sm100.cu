@@ -347,7 +347,7 @@ cudaError_t launch(const Fp8GemmArgs &a, int num_sms, cudaStream_t s)
     const GemmArgs g = gemm_args(a, out_cols<EPI>());
     // every slice may end inside a tile
     const int64_t most = (a.rows / BM + min64(a.E, a.rows)) * g.n_tiles;
-    if (most >= (static_cast<int64_t>(1) << 31)) return cudaErrorInvalidValue;
+    if (most > (static_cast<int64_t>(1) << 30)) return cudaErrorInvalidValue;  // tile numbers and a step
     const dim3 grid(static_cast<unsigned>(min64(most, num_sms)));
     return launch_k(kernel, grid, dim3(THREADS), kSmemBytes, s, tmA, tmW, tmW3, g);
 }

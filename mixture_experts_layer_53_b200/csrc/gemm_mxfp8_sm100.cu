@@ -442,11 +442,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                     t_ahead += step;
                 }
             };
-            // exponent codes; a scale that is no power of two (zero,
-            // negative, any mantissa) is reported
+            // exponent codes; a scale that is no power of two and no NaN
+            // (zero, negative, infinite, any mantissa) is reported
             auto code = [&](float v) {
                 const uint32_t b = __float_as_uint(v), e = b >> 23;
-                odd_scale |= e == 0 || e > 255 || (e < 255 && (b & 0x7FFFFFu) != 0);
+                odd_scale |= e == 0 || e > 255 || (e < 255) == ((b & 0x7FFFFFu) != 0);
                 return e & 255u;
             };
             for (int i = 0; i + 1 < AHEAD; ++i) fetch(ctl->ahead[atom][i]);
@@ -721,7 +721,7 @@ cudaError_t launch(const Fp8GemmArgs &a, int num_sms, cudaStream_t s, int ranks 
     if (err != cudaSuccess) return err;
     const GemmArgs g = gemm_args(a, TILE_N);
     const int64_t most = most_tiles<S>(a, g.n_tiles);
-    if (most * ranks >= (static_cast<int64_t>(1) << 31)) return cudaErrorInvalidValue;
+    if (most * ranks > (static_cast<int64_t>(1) << 30)) return cudaErrorInvalidValue;  // tile numbers and a step
     const dim3 grid(static_cast<unsigned>(SPLIT ? most * ranks : min64(most, num_sms)));
     return launch_clusters(kernel, grid, dim3(THREADS), ranks, smem_bytes<S>(), s, tmA, tmW, tmW3, g);
 }

@@ -24,7 +24,7 @@ def lib():
 
 
 @pytest.mark.parametrize("args,code", [
-    ((2, A, 4, 64, A, A), 1), ((0, A, -1, 64, A, A), 1), ((0, A, 4, 0, A, A), 1), ((0, A, 4, 24, A, A), 2),
+    ((2, A, 4, 64, A, A), 1), ((0, A, -1, 64, A, A), 1), ((0, A, 4, 0, A, A), 1), ((0, A, 4, 24, A, A), 2), ((0, A, 4, 2 ** 30 + 16, A, A), 2),
     ((0, A, 2 ** 31, 64, A, A), 2), ((1, None, 4, 64, A, A), 1), ((1, OFF, 4, 64, A, A), 1),
     ((1, A, 4, 64, None, A), 1), ((1, A, 4, 64, A, OFF), 1), ((1, None, 0, 64, None, None), 0),
 ])
@@ -45,7 +45,8 @@ def test_quantize_weights(lib, args, code):
 @pytest.mark.parametrize("change,code", [
     (dict(rows=-1), 1), (dict(n=0), 1), (dict(k=0), 1), (dict(E=0), 1), (dict(E=257), 2), (dict(n=40), 2),
     (dict(k=40), 2), (dict(rows=2 ** 31), 2), (dict(dt=2), 1), (dict(any=2), 1), (dict(a=None), 1), (dict(a=OFF), 1), (dict(asc=None), 1),
-    (dict(off=None), 1), (dict(w=OFF), 1), (dict(wsc=None), 1), (dict(out=None), 1), (dict(out=OFF), 1),
+    (dict(off=None), 1), (dict(off=ctypes.c_void_p(0x10002)), 1), (dict(n=2 ** 30 + 16), 2), (dict(k=2 ** 30 + 16), 2),
+    (dict(w=OFF), 1), (dict(wsc=None), 1), (dict(out=None), 1), (dict(out=OFF), 1),
     (dict(rows=0, a=None, asc=None, out=None), 0),
 ])
 def test_matmul(lib, change, code):
@@ -80,6 +81,7 @@ def test_ffn(lib):
     (dict(dt=2), 1), (dict(scores=2), 1), (dict(z=None), 1), (dict(z=OFF), 1), (dict(ids=None), 1), (dict(N=-1), 1),
     (dict(E=0), 1), (dict(E=257), 2), (dict(k=0), 1), (dict(k=9), 1), (dict(E=64, k=17), 2), (dict(S=0), 1),
     (dict(seq=None, S=3), 1), (dict(loss=None), 1), (dict(counts=None), 1), (dict(weight=None), 1), (dict(ws=None), 4),
+    (dict(loss=ctypes.c_void_p(0x10002)), 1), (dict(ids=ctypes.c_void_p(0x10001)), 1), (dict(seq=ctypes.c_void_p(0x10003)), 1),
     (dict(ws=OFF), 4), (dict(size=ctypes.c_size_t(8)), 4), (dict(N=2 ** 31 - 1, k=2), 2),
 ])
 def test_balance_loss(lib, change, code):
@@ -92,7 +94,7 @@ def test_balance_loss(lib, change, code):
 @pytest.mark.parametrize("change,code", [
     (dict(dt=3), 1), (dict(scores=-1), 1), (dict(z=None), 1), (dict(E=300), 2), (dict(seq=None), 1),
     (dict(counts=None), 1), (dict(weight=None), 1), (dict(coef=F(float("nan"))), 1), (dict(dz=None), 1),
-    (dict(dz=OFF), 1), (dict(N=0, z=None, dz=None), 0),
+    (dict(dz=OFF), 1), (dict(dloss=ctypes.c_void_p(0x10002)), 1), (dict(N=0, z=None, dz=None), 0),
 ])
 def test_balance_loss_backward(lib, change, code):
     a = dict(dt=0, scores=0, z=A, seq=A, mask=None, N=64, E=8, S=4, counts=A, weight=A, coef=F(1.0), dloss=None, dz=A)

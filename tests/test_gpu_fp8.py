@@ -195,7 +195,7 @@ def test_scales_of_many_sizes():
 def test_scales_that_are_no_powers_of_two_are_reported():
     a, w, off = _operands([20, 30], 64, 272, seed=5)
     for scales, at in ((a[1], (1, 45)), (w[1], (1, 0, 2))):
-        for bad in (1.5, 0.0, -1.0, 1e-40):
+        for bad in (1.5, 0.0, -1.0, 1e-40, float("inf")):
             keep = float(scales[at])
             scales[at] = bad
             status = torch.zeros(1, dtype=torch.int32, device=DEV)
@@ -260,6 +260,43 @@ def test_input_gradient(lengths, n, k):
     vv = R.row_values(np64(v[0]), np64(v[1]))
     _, pbound = R.product(vv, Wv, off.cpu().numpy())
     assert abs((dyv * np64(pv)).sum() - (np64(dx) * vv).sum()) <= (np.abs(dyv) * pbound).sum() + (bound * np.abs(vv)).sum()
+
+
+def test_offsets_beyond_32_bits():
+    """Operands and results of more than 2^31 values: the last rows and experts are where they belong."""
+    rows, cols = 300_000, 7168
+    x = torch.zeros((rows, cols), dtype=BF, device=DEV)
+    x[-3:] = torch.randn((3, cols), generator=gen(1), device=DEV)
+    q, s = M.moe_quantize_rows(x)
+    wq, ws = R.quantize_rows(np64(x[-3:]))
+    assert np.array_equal(np64(q[-3:]), wq) and np.array_equal(np64(s[:, -3:]), ws)
+    assert not q[:-3].view(torch.uint8).any()
+    del x, q, s
+    W = torch.zeros((256, 2048, 4112), dtype=BF, device=DEV)
+    W[-1] = torch.randn((2048, 4112), generator=gen(2), device=DEV)
+    for t in (False, True):
+        q, s = M.moe_quantize_weights(W, transpose=t)
+        wq, ws = R.quantize_weights(np64(W[-1:]), t)
+        assert np.array_equal(np64(q[-1:]), wq) and np.array_equal(np64(s[-1:]), ws)
+        assert not q[:-1].view(torch.uint8).any()
+    a = M.moe_quantize_rows(torch.randn((5, 2048), generator=gen(3), device=DEV))
+    off = torch.full((257,), 3, dtype=torch.int32, device=DEV)
+    off[0], off[256] = 0, 5                       # three rows of the first expert, two of the last
+    y = M.moe_expert_matmul_fp8(a, off, (q, s), out_dtype=F32)
+    want, bound = R.product(R.row_values(np64(a[0]), np64(a[1]))[3:], R.weight_values(wq, ws), [0, 2])
+    checked(y[3:], want, bound)
+    assert not y[:3].any()
+    del W, q, s
+    rows = 1_100_000
+    a = M.moe_quantize_rows(torch.randn((rows, 16), generator=gen(4), device=DEV))
+    w = M.moe_quantize_weights(torch.randn((2, 2048, 16), generator=gen(5), device=DEV))
+    off = torch.tensor([0, rows - 77, rows], dtype=torch.int32, device=DEV)
+    for free in (False, True):
+        y = M.moe_expert_matmul_fp8(a, off, w, any_scales=free)
+        av, wv = R.row_values(np64(a[0][-300:]), np64(a[1][:, -300:])), R.weight_values(np64(w[0]), np64(w[1]))
+        want, bound = R.product(av, wv, [0, 223, 300])
+        checked(y[-300:], want, bound + R.UBF * (np.abs(want) + bound))
+        del y
 
 
 # ---------------------------------------------------------------------- FFN
