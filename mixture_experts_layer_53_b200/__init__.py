@@ -489,8 +489,8 @@ def moe_quantize_rows(x: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch
     dtype, dev = _float_dtype(where, "x", x), x.device
     rows, cols = x.shape
     with _on(where, x, stream):
-        q = torch.empty((rows, cols), dtype=_E4M3, device=dev)
-        scales = torch.empty((_fp8_blocks(cols), rows), dtype=_F32, device=dev)
+        q = torch.empty_like(x, dtype=_E4M3)
+        scales = x.new_empty((_fp8_blocks(cols), rows), dtype=_F32)
         rc = library().moe_quantize_rows(dtype, x.data_ptr(), rows, cols, q.data_ptr(), scales.data_ptr(),
                                          _raw_stream(dev))
     _check(rc, where)
@@ -647,7 +647,7 @@ def moe_balance_loss_backward(logits: torch.Tensor, fwd: Dict[str, torch.Tensor]
     N, E, S, off, mask = _sequences(where, logits, seq_offsets, token_mask)
     dtype = _float_dtype(where, "logits", logits)
     with _on(where, logits, stream):
-        dlogits = torch.empty((N, E), dtype=_F32, device=dev)
+        dlogits = torch.empty_like(logits, dtype=_F32)
         rc = library().moe_balance_loss_backward(
             dtype, SCORES[scores], logits.data_ptr(), off, mask, N, E, S,
             _arg(where, "counts", fwd["counts"], _I32, (S, E), dev),
