@@ -37,6 +37,7 @@ struct GemmArgs {
     int32_t *status;
     int64_t rows;
     int E, K, n_out, n_tiles;
+    int early;               // offsets and weights are older than the stream's previous kernel
 };
 
 inline GemmArgs gemm_args(const Fp8GemmArgs &a, int tile_n)
@@ -55,6 +56,7 @@ inline GemmArgs gemm_args(const Fp8GemmArgs &a, int tile_n)
     g.K = a.k;
     g.n_out = a.n;
     g.n_tiles = (a.n + tile_n - 1) / tile_n;
+    g.early = a.early;
     return g;
 }
 

@@ -260,7 +260,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     // nothing above touches memory that an earlier kernel writes
     const int ranks = SPLIT ? static_cast<int>(cluster_nctas()) : 1, rank = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
-    pdl_enter();
+    // The stream's previous kernel may have written the slices and the weights
+    // (then wait for it here) or, inside an FFN, only the rows: then what does
+    // not depend on it starts now, and every warp waits before its part.
+    if (!g.early) pdl_enter();
+    auto begin = [&] {
+        if (g.early) pdl_enter();
+    };
     tc_fence_before();
     load_slices<S::NMAX>(&ctl->slices, g);
     tc_fence_after();
@@ -287,25 +293,41 @@ __global__ void __launch_bounds__(THREADS, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(ROLE_REGS));
         if (warp == 0 && lane == 0) {
             // ------------------------------------------------ TMA producer
-            int stage = 0;
+            int stage = 0, ahead = 0;  // ahead: stages whose weights are on their way
             uint32_t phase = 0, armed = 0, armed_parity = 0;
             bool ok = true;
+            auto load_weights = [&](int e, int n0, int n, int kb, int to) {
+                uint8_t *sW = tiles + to * S::STAGE;
+                uint64_t *full = &ctl->full[to];
+                mbar_arrive_expect_tx(full, static_cast<uint32_t>(S::W_BYTES + n * BK));
+                armed |= 1u << to;
+                armed_parity = (armed_parity & ~(1u << to)) | (phase << to);
+                tma_load_3d(sW, &tmW, full, kb * BK, n0, e);
+                if (EPI == EPI_SWIGLU) tma_load_3d(sW + WM * BK, &tmW3, full, kb * BK, n0, e);
+            };
+            if (g.early && first < total) {
+                const Tile ti = decode_tile(first, sl, g.E, g.n_tiles);
+                const int n = (rows_of(ti).count + 15) & ~15;
+                for (; ahead < min(S::STAGES, kb_hi - kb_lo); ++ahead)
+                    load_weights(ti.e, ti.n_tile * TILE_N, n, kb_lo + ahead, ahead);
+            }
+            begin();
             for (int t = first; t < total && ok; t += step) {
                 const Tile ti = decode_tile(t, sl, g.E, g.n_tiles);
                 const Rows tr = rows_of(ti);
                 const int row0 = tr.first, n0 = ti.n_tile * TILE_N, n = (tr.count + 15) & ~15;
                 for (int kb = kb_lo; kb < kb_hi; ++kb) {
-                    if (!mbar_wait(&ctl->empty[stage], phase ^ 1u, abort_flag, g.status)) {
-                        ok = false;
-                        break;
+                    if (ahead > 0) {
+                        --ahead;
+                    } else {
+                        if (!mbar_wait(&ctl->empty[stage], phase ^ 1u, abort_flag, g.status)) {
+                            ok = false;
+                            break;
+                        }
+                        load_weights(ti.e, n0, n, kb, stage);
                     }
-                    uint8_t *sW = tiles + stage * S::STAGE, *sA = sW + S::W_BYTES;
+                    uint8_t *sA = tiles + stage * S::STAGE + S::W_BYTES;
                     uint64_t *full = &ctl->full[stage];
-                    mbar_arrive_expect_tx(full, static_cast<uint32_t>(S::W_BYTES + n * BK));
-                    armed |= 1u << stage;
-                    armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-                    tma_load_3d(sW, &tmW, full, kb * BK, n0, ti.e);
-                    if (EPI == EPI_SWIGLU) tma_load_3d(sW + WM * BK, &tmW3, full, kb * BK, n0, ti.e);
                     int r = 0;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -329,6 +351,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         } else if (warp == 1 && lane == 0) {
             // -------------------------------------------------- MMA issuer
+            begin();
             int stage = 0, buf = 0;
             uint32_t phase = 0, tphase = 0, group = 0;
             bool ok = true, issued = false;
@@ -401,6 +424,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         } else if (warp >= 2 && warp - 2 < S::ATOMS) {
             // ------------------------------------------------------ scales
+            begin();
             const int atom = warp - 2;
             const int nblocks = (g.n_out + kFp8Block - 1) / kFp8Block;
             bool odd_scale = false;
@@ -495,6 +519,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SUM_REGS));
         // ---------------------------------------------------- epilogue
+        begin();
         const int quarter = warp & 3, half = (warp - FIRST_SUM_WARP) >> 2;
         int buf = 0;
         uint32_t tphase = 0, xphase = 0;

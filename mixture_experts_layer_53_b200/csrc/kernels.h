@@ -360,6 +360,7 @@ struct Fp8GemmArgs {
     int32_t *status;
     int64_t rows;
     int E, n, k;
+    int early;              // offsets and weights are not written by the stream's previous kernel
 };
 // any scales (gemm_fp8_sm100.cu), and scales that are powers of two
 // (gemm_mxfp8_sm100.cu: other values are reported in *status)

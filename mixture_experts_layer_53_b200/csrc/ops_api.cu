@@ -184,6 +184,7 @@ moe_status moe_expert_ffn_fp8(const moe_config *cfg, const void *x_sorted, const
         g.E = cfg->E;
         g.n = cfg->d_ff;
         g.k = cfg->d_model;
+        g.early = 1;  // each product follows a kernel of this call, which writes only its rows
         if ((err = product(w->any_scales, g, s)) != cudaSuccess) return record_cuda_error(err);
         g.epi = kFp8Bf16;
         g.a = base + L.hq;
