@@ -8,7 +8,7 @@
 namespace moe {
 
 // Device-side status codes (same values as moe_status in moe.h).
-enum : int32_t { kDevOk = 0, kDevBadArgument = 1, kDevTimeout = 5, kDevBadExpertId = 6 };
+enum : int32_t { kDevOk = 0, kDevTimeout = 5, kDevBadExpertId = 6 };
 
 // Tokens handled by one router CTA; also the dispatch chunk (chunk c holds
 // tokens [c*kChunkTokens, (c+1)*kChunkTokens) and their assignments).

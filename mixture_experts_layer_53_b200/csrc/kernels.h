@@ -7,6 +7,10 @@
 
 namespace moe {
 
+// Device-side status code of a bad argument found on the device (MOE_ERR_INVALID_ARG
+// of moe.h; the others are in common.cuh).
+enum : int32_t { kDevBadArgument = 1 };
+
 // dtype / router / activation codes are those of moe.h.
 enum { kF32 = 0, kBF16 = 1 };
 enum { kSoftmaxTopk = 0, kTopkSoftmax = 1, kSigmoid = 2 };
