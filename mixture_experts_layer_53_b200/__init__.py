@@ -20,7 +20,6 @@ loss, aux-free bias" (sec. 2): N, E, k, d_model, d_ff, W_g, b_e.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Dict, Optional, Sequence, Tuple
@@ -417,7 +416,6 @@ def moe_backward(cfg: MoeConfig, x: torch.Tensor, W_g: torch.Tensor, W1: torch.T
 # bindings keep the host's part short: pointers and streams go to ctypes as
 # plain integers, and a device or stream is made current only where it is not.
 
-_HERE = contextlib.nullcontext()
 _E4M3, _F32, _BF16, _I32 = torch.float8_e4m3fn, torch.float32, torch.bfloat16, torch.int32
 
 
@@ -425,8 +423,9 @@ def _fp8_blocks(n: int) -> int:
     return -(-n // 128)
 
 
-def _on(where: str, t: torch.Tensor, stream):
-    """The device of t, and the given stream, current for a call's allocations and launches."""
+def _elsewhere(where: str, t: torch.Tensor, stream):
+    """None if a call on t can allocate and launch as things stand, else a context in which it can: the given
+    stream, and the device of t, current."""
     dev = t.device
     if dev.type != "cuda":
         raise ValueError(f"{where}: tensor arguments must live on a CUDA device")
@@ -434,7 +433,7 @@ def _on(where: str, t: torch.Tensor, stream):
         if stream.device != dev:
             raise ValueError(f"{where}: stream of {stream.device} for tensors on {dev}")
         return torch.cuda.stream(stream)
-    return _HERE if dev.index == torch._C._cuda_getDevice() else torch.cuda.device(dev)
+    return None if dev.index == torch._C._cuda_getDevice() else torch.cuda.device(dev)
 
 
 def _raw_stream(dev: torch.device) -> int:
@@ -488,11 +487,14 @@ def moe_quantize_rows(x: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch
         raise ValueError(f"{where}: x must be [rows, cols]")
     dtype, dev = _float_dtype(where, "x", x), x.device
     rows, cols = x.shape
-    with _on(where, x, stream):
-        q = torch.empty_like(x, dtype=_E4M3)
-        scales = x.new_empty((_fp8_blocks(cols), rows), dtype=_F32)
-        rc = library().moe_quantize_rows(dtype, x.data_ptr(), rows, cols, q.data_ptr(), scales.data_ptr(),
-                                         _raw_stream(dev))
+    there = _elsewhere(where, x, stream)
+    if there is not None:
+        with there:
+            return moe_quantize_rows(x)
+    q = torch.empty_like(x, dtype=_E4M3)
+    scales = x.new_empty((_fp8_blocks(cols), rows), dtype=_F32)
+    rc = library().moe_quantize_rows(dtype, x.data_ptr(), rows, cols, q.data_ptr(), scales.data_ptr(),
+                                     _raw_stream(dev))
     _check(rc, where)
     return q, scales
 
@@ -506,11 +508,14 @@ def moe_quantize_weights(W: torch.Tensor, transpose: bool = False, stream=None) 
     dtype, dev = _float_dtype(where, "W", W), W.device
     E, rows, cols = W.shape
     r, c = (cols, rows) if transpose else (rows, cols)
-    with _on(where, W, stream):
-        q = torch.empty((E, r, c), dtype=_E4M3, device=dev)
-        scales = torch.empty((E, _fp8_blocks(r), _fp8_blocks(c)), dtype=_F32, device=dev)
-        rc = library().moe_quantize_weights(dtype, W.data_ptr(), E, rows, cols, int(bool(transpose)), q.data_ptr(),
-                                            scales.data_ptr(), _raw_stream(dev))
+    there = _elsewhere(where, W, stream)
+    if there is not None:
+        with there:
+            return moe_quantize_weights(W, transpose)
+    q = torch.empty((E, r, c), dtype=_E4M3, device=dev)
+    scales = torch.empty((E, _fp8_blocks(r), _fp8_blocks(c)), dtype=_F32, device=dev)
+    rc = library().moe_quantize_weights(dtype, W.data_ptr(), E, rows, cols, int(bool(transpose)), q.data_ptr(),
+                                        scales.data_ptr(), _raw_stream(dev))
     _check(rc, where)
     return q, scales
 
@@ -532,16 +537,19 @@ def moe_expert_matmul_fp8(a: Tuple[torch.Tensor, torch.Tensor], offsets: torch.T
     kb = _fp8_blocks(k)
     if out_dtype is not _BF16 and out_dtype is not _F32:
         raise ValueError(f"{where}: out_dtype must be bfloat16 or float32, got {out_dtype}")
-    with _on(where, aq, stream):
-        if out is None:
-            out = torch.empty((rows, n), dtype=out_dtype, device=dev)
-        rc = library().moe_expert_matmul_fp8(
-            rows, n, k, E, _arg(where, "a", aq, _E4M3, (rows, k), dev),
-            _arg(where, "a's scales", asc, _F32, (kb, rows), dev),
-            _arg(where, "offsets", offsets, _I32, (E + 1,), dev), _arg(where, "w", wq, _E4M3, (E, n, k), dev),
-            _arg(where, "w's scales", wsc, _F32, (E, _fp8_blocks(n), kb), dev), int(bool(any_scales)),
-            int(out_dtype is _BF16), _arg(where, "out", out, out_dtype, (rows, n), dev),
-            None if status is None else _arg(where, "status", status, _I32, (1,), dev), _raw_stream(dev))
+    there = _elsewhere(where, aq, stream)
+    if there is not None:
+        with there:
+            return moe_expert_matmul_fp8(a, offsets, w, out_dtype, out, any_scales, status)
+    if out is None:
+        out = torch.empty((rows, n), dtype=out_dtype, device=dev)
+    rc = library().moe_expert_matmul_fp8(
+        rows, n, k, E, _arg(where, "a", aq, _E4M3, (rows, k), dev),
+        _arg(where, "a's scales", asc, _F32, (kb, rows), dev),
+        _arg(where, "offsets", offsets, _I32, (E + 1,), dev), _arg(where, "w", wq, _E4M3, (E, n, k), dev),
+        _arg(where, "w's scales", wsc, _F32, (E, _fp8_blocks(n), kb), dev), int(bool(any_scales)),
+        int(out_dtype is _BF16), _arg(where, "out", out, out_dtype, (rows, n), dev),
+        None if status is None else _arg(where, "status", status, _I32, (1,), dev), _raw_stream(dev))
     _check(rc, where)
     return out
 
@@ -566,24 +574,27 @@ def moe_expert_ffn_fp8(cfg: MoeConfig, x_sorted: torch.Tensor, offsets: torch.Te
     where, dev = "moe_expert_ffn_fp8", x_sorted.device
     E, d, F, A = cfg.E, cfg.d_model, cfg.d_ff, cfg.N * cfg.k
     db, Fb = _fp8_blocks(d), _fp8_blocks(F)
-    with _on(where, x_sorted, stream):
-        if ws is None:
-            ws = moe_expert_ffn_fp8_workspace(cfg, dev)
-        if out is None:
-            out = torch.empty((A, d), dtype=_BF16, device=dev)
-        w = Fp8Experts(
-            _arg(where, "W1", W1[0], _E4M3, (E, F, d), dev), _arg(where, "W1's scales", W1[1], _F32, (E, Fb, db), dev),
-            None if W3 is None else _arg(where, "W3", W3[0], _E4M3, (E, F, d), dev),
-            None if W3 is None else _arg(where, "W3's scales", W3[1], _F32, (E, Fb, db), dev),
-            _arg(where, "W2", W2[0], _E4M3, (E, d, F), dev), _arg(where, "W2's scales", W2[1], _F32, (E, db, Fb), dev),
-            None if b1 is None else _arg(where, "b1", b1, _BF16, (E, F), dev),
-            None if b2 is None else _arg(where, "b2", b2, _BF16, (E, d), dev), int(bool(any_scales)))
-        rc = library().moe_expert_ffn_fp8(
-            ctypes.byref(cfg), _arg(where, "x_sorted", x_sorted, _BF16, (A, d), dev),
-            _arg(where, "offsets", offsets, _I32, (E + 1,), dev), ctypes.byref(w),
-            _arg(where, "out", out, _BF16, (A, d), dev),
-            None if status is None else _arg(where, "status", status, _I32, (1,), dev),
-            *_workspace_arg(where, ws, dev), _raw_stream(dev))
+    there = _elsewhere(where, x_sorted, stream)
+    if there is not None:
+        with there:
+            return moe_expert_ffn_fp8(cfg, x_sorted, offsets, W1, W2, b1, W3, b2, ws, status, out, any_scales)
+    if ws is None:
+        ws = moe_expert_ffn_fp8_workspace(cfg, dev)
+    if out is None:
+        out = torch.empty((A, d), dtype=_BF16, device=dev)
+    w = Fp8Experts(
+        _arg(where, "W1", W1[0], _E4M3, (E, F, d), dev), _arg(where, "W1's scales", W1[1], _F32, (E, Fb, db), dev),
+        None if W3 is None else _arg(where, "W3", W3[0], _E4M3, (E, F, d), dev),
+        None if W3 is None else _arg(where, "W3's scales", W3[1], _F32, (E, Fb, db), dev),
+        _arg(where, "W2", W2[0], _E4M3, (E, d, F), dev), _arg(where, "W2's scales", W2[1], _F32, (E, db, Fb), dev),
+        None if b1 is None else _arg(where, "b1", b1, _BF16, (E, F), dev),
+        None if b2 is None else _arg(where, "b2", b2, _BF16, (E, d), dev), int(bool(any_scales)))
+    rc = library().moe_expert_ffn_fp8(
+        ctypes.byref(cfg), _arg(where, "x_sorted", x_sorted, _BF16, (A, d), dev),
+        _arg(where, "offsets", offsets, _I32, (E + 1,), dev), ctypes.byref(w),
+        _arg(where, "out", out, _BF16, (A, d), dev),
+        None if status is None else _arg(where, "status", status, _I32, (1,), dev),
+        *_workspace_arg(where, ws, dev), _raw_stream(dev))
     _check(rc, where)
     return out
 
@@ -619,20 +630,23 @@ def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, seq_offsets: 
     if topk_ids.dim() != 2:
         raise ValueError(f"{where}: topk_ids must be [N, k]")
     k, lib = topk_ids.shape[1], library()
-    with _on(where, logits, stream):
-        if ws is None:
-            n = lib.moe_balance_loss_workspace_size(N, E, S)
-            if n == 0:
-                raise MoeError(2, "moe_balance_loss_workspace_size")
-            ws = _aligned_bytes(n, dev)
-        loss = torch.empty(1, dtype=_F32, device=dev)
-        counts = torch.empty((S, E), dtype=_I32, device=dev)
-        weight = torch.empty(S, dtype=_F32, device=dev)
-        status = torch.empty(1, dtype=_I32, device=dev)
-        rc = lib.moe_balance_loss(dtype, SCORES[scores], logits.data_ptr(),
-                                  _arg(where, "topk_ids", topk_ids, _I32, (N, k), dev), off, mask, N, E, k, S,
-                                  loss.data_ptr(), counts.data_ptr(), weight.data_ptr(), status.data_ptr(),
-                                  *_workspace_arg(where, ws, dev), _raw_stream(dev))
+    there = _elsewhere(where, logits, stream)
+    if there is not None:
+        with there:
+            return moe_balance_loss(logits, topk_ids, seq_offsets, token_mask, scores, ws)
+    if ws is None:
+        n = lib.moe_balance_loss_workspace_size(N, E, S)
+        if n == 0:
+            raise MoeError(2, "moe_balance_loss_workspace_size")
+        ws = _aligned_bytes(n, dev)
+    loss = torch.empty(1, dtype=_F32, device=dev)
+    counts = torch.empty((S, E), dtype=_I32, device=dev)
+    weight = torch.empty(S, dtype=_F32, device=dev)
+    status = torch.empty(1, dtype=_I32, device=dev)
+    rc = lib.moe_balance_loss(dtype, SCORES[scores], logits.data_ptr(),
+                              _arg(where, "topk_ids", topk_ids, _I32, (N, k), dev), off, mask, N, E, k, S,
+                              loss.data_ptr(), counts.data_ptr(), weight.data_ptr(), status.data_ptr(),
+                              *_workspace_arg(where, ws, dev), _raw_stream(dev))
     _check(rc, where)
     return {"loss": loss, "counts": counts, "seq_weight": weight, "status": status}
 
@@ -646,14 +660,17 @@ def moe_balance_loss_backward(logits: torch.Tensor, fwd: Dict[str, torch.Tensor]
     where, dev = "moe_balance_loss_backward", logits.device
     N, E, S, off, mask = _sequences(where, logits, seq_offsets, token_mask)
     dtype = _float_dtype(where, "logits", logits)
-    with _on(where, logits, stream):
-        dlogits = torch.empty_like(logits, dtype=_F32)
-        rc = library().moe_balance_loss_backward(
-            dtype, SCORES[scores], logits.data_ptr(), off, mask, N, E, S,
-            _arg(where, "counts", fwd["counts"], _I32, (S, E), dev),
-            _arg(where, "seq_weight", fwd["seq_weight"], _F32, (S,), dev), coef,
-            None if dloss is None else _arg(where, "dloss", dloss, _F32, (1,), dev), dlogits.data_ptr(),
-            _raw_stream(dev))
+    there = _elsewhere(where, logits, stream)
+    if there is not None:
+        with there:
+            return moe_balance_loss_backward(logits, fwd, seq_offsets, token_mask, scores, coef, dloss)
+    dlogits = torch.empty_like(logits, dtype=_F32)
+    rc = library().moe_balance_loss_backward(
+        dtype, SCORES[scores], logits.data_ptr(), off, mask, N, E, S,
+        _arg(where, "counts", fwd["counts"], _I32, (S, E), dev),
+        _arg(where, "seq_weight", fwd["seq_weight"], _F32, (S,), dev), coef,
+        None if dloss is None else _arg(where, "dloss", dloss, _F32, (1,), dev), dlogits.data_ptr(),
+        _raw_stream(dev))
     _check(rc, where)
     return dlogits
 
