@@ -463,7 +463,8 @@ MOE_API moe_status moe_permute_rows(int32_t dtype, const void *src, const int32_
  *   activations  q [rows, cols] e4m3,    scales [ceil(cols/128), rows] f32
  *   weights      q [E, rows, cols] e4m3, scales [E, ceil(rows/128), ceil(cols/128)] f32
  * Limits: rows of activations < 2^31; widths multiples of 16, at most 2^30
- * (else MOE_ERR_UNSUPPORTED); every pointer but offsets 16-byte aligned.
+ * (else MOE_ERR_UNSUPPORTED); offsets and scales 4-byte aligned (one expert's
+ * part of a scale tensor need not start on 16 bytes), other pointers 16.
  */
 
 /* Quantises activations x [rows, cols] (dtype MOE_F32 or MOE_BF16). */
@@ -557,6 +558,8 @@ MOE_API size_t moe_balance_loss_workspace_size(int64_t N, int32_t E, int32_t S);
  * MOE_ERR_BAD_EXPERT_ID for an id outside [0, E) of a counted token, which is
  * left out; MOE_ERR_INVALID_ARG for seq_offsets that decrease or leave 0 .. N
  * (the other outputs are then meaningless).  E <= 256, k <= min(E, 16), N k < 2^31.
+ * logits (and dlogits below) start on a multiple of four of their values if
+ * E is one, else of one; the other pointers on 4 bytes, ws on 256.
  */
 MOE_API moe_status moe_balance_loss(int32_t dtype, int32_t scores, const void *logits, const int32_t *topk_ids,
                                     const int32_t *seq_offsets, const uint8_t *token_mask, int64_t N, int32_t E,

@@ -20,6 +20,12 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool given(const void *p) { return p != nullptr && aligned16(p); }
 bool given4(const void *p) { return p != nullptr && aligned4(p); }
+// Rows of E values are read four at a time if E is a multiple of four.
+bool given_rows(const void *p, int32_t dtype, int32_t E)
+{
+    const uintptr_t es = dtype == MOE_F32 ? 4 : 2;
+    return p != nullptr && reinterpret_cast<uintptr_t>(p) % (E % 4 == 0 ? 4 * es : es) == 0;
+}
 constexpr int64_t kMaxRows = static_cast<int64_t>(1) << 31;
 constexpr int32_t kMaxWidth = 1 << 30;  // 32-bit column arithmetic keeps room for a tile
 
@@ -90,7 +96,7 @@ moe_status moe_quantize_rows(int32_t dtype, const void *x, int64_t rows, int32_t
         if (rows < 0 || cols <= 0) return MOE_ERR_INVALID_ARG;
         if (cols % 16 != 0 || cols > kMaxWidth || rows >= kMaxRows) return MOE_ERR_UNSUPPORTED;
         if (rows == 0) return MOE_OK;
-        if (!given(x) || !given(q) || !given(scales)) return MOE_ERR_INVALID_ARG;
+        if (!given(x) || !given(q) || !given4(scales)) return MOE_ERR_INVALID_ARG;
         return done(launch_quantize_rows(dtype, x, rows, cols, q, scales, reinterpret_cast<cudaStream_t>(stream)));
     });
 }
@@ -103,7 +109,7 @@ moe_status moe_quantize_weights(int32_t dtype, const void *W, int32_t E, int32_t
         if (E <= 0 || rows <= 0 || cols <= 0 || (transpose != 0 && transpose != 1)) return MOE_ERR_INVALID_ARG;
         if (rows % 16 != 0 || cols % 16 != 0 || rows > kMaxWidth || cols > kMaxWidth) return MOE_ERR_UNSUPPORTED;
         if (static_cast<int64_t>(E) * fp8_blocks(rows) * fp8_blocks(cols) >= kMaxRows) return MOE_ERR_UNSUPPORTED;
-        if (!given(W) || !given(q) || !given(scales)) return MOE_ERR_INVALID_ARG;
+        if (!given(W) || !given(q) || !given4(scales)) return MOE_ERR_INVALID_ARG;
         return done(launch_quantize_weights(dtype, W, E, rows, cols, transpose, q, scales,
                                             reinterpret_cast<cudaStream_t>(stream)));
     });
@@ -119,9 +125,9 @@ moe_status moe_expert_matmul_fp8(int64_t rows, int32_t n, int32_t k, int32_t E, 
         if (rows < 0 || n <= 0 || k <= 0 || E <= 0 || (any_scales != 0 && any_scales != 1)) return MOE_ERR_INVALID_ARG;
         if (E > kMaxE || n % 16 != 0 || k % 16 != 0 || n > kMaxWidth || k > kMaxWidth || rows >= kMaxRows)
             return MOE_ERR_UNSUPPORTED;
-        if (!given4(offsets) || !aligned4(dev_status) || !given(w_q) || !given(w_scales)) return MOE_ERR_INVALID_ARG;
+        if (!given4(offsets) || !aligned4(dev_status) || !given(w_q) || !given4(w_scales)) return MOE_ERR_INVALID_ARG;
         if (rows == 0) return MOE_OK;
-        if (!given(a_q) || !given(a_scales) || !given(out)) return MOE_ERR_INVALID_ARG;
+        if (!given(a_q) || !given4(a_scales) || !given(out)) return MOE_ERR_INVALID_ARG;
         Fp8GemmArgs g{};
         g.epi = out_dtype == MOE_F32 ? kFp8F32 : kFp8Bf16;
         g.a = a_q;
@@ -154,8 +160,8 @@ moe_status moe_expert_ffn_fp8(const moe_config *cfg, const void *x_sorted, const
         const bool swiglu = cfg->act == MOE_ACT_SWIGLU;
         if (!given4(offsets) || !aligned4(dev_status) || !w) return MOE_ERR_INVALID_ARG;
         if (cfg->N > 0 && (!given(x_sorted) || !given(y_sorted))) return MOE_ERR_INVALID_ARG;
-        if (!given(w->W1) || !given(w->W1_scales) || !given(w->W2) || !given(w->W2_scales)) return MOE_ERR_INVALID_ARG;
-        if (swiglu ? (!given(w->W3) || !given(w->W3_scales) || w->b1) : (w->W3 || w->W3_scales)) return MOE_ERR_INVALID_ARG;
+        if (!given(w->W1) || !given4(w->W1_scales) || !given(w->W2) || !given4(w->W2_scales)) return MOE_ERR_INVALID_ARG;
+        if (swiglu ? (!given(w->W3) || !given4(w->W3_scales) || w->b1) : (w->W3 || w->W3_scales)) return MOE_ERR_INVALID_ARG;
         if (!aligned16(w->b1) || !aligned16(w->b2)) return MOE_ERR_INVALID_ARG;
         if (w->any_scales != 0 && w->any_scales != 1) return MOE_ERR_INVALID_ARG;
         const FfnLayout L = ffn_layout(cfg);
@@ -218,7 +224,7 @@ moe_status moe_balance_loss(int32_t dtype, int32_t scores, const void *logits, c
         if (k <= 0 || k > E) return MOE_ERR_INVALID_ARG;
         if (k > kMaxK || N * k >= kMaxRows) return MOE_ERR_UNSUPPORTED;
         if (!seq_offsets && S != 1) return MOE_ERR_INVALID_ARG;
-        if (N > 0 && (!given(logits) || !given4(topk_ids))) return MOE_ERR_INVALID_ARG;
+        if (N > 0 && (!given_rows(logits, dtype, E) || !given4(topk_ids))) return MOE_ERR_INVALID_ARG;
         if (!given4(loss_out) || !given4(counts_out) || !given4(seq_weight_out)) return MOE_ERR_INVALID_ARG;
         if (!aligned4(seq_offsets) || !aligned4(dev_status)) return MOE_ERR_INVALID_ARG;
         if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 || ws_bytes < balance_workspace(N, E, S))
@@ -254,7 +260,8 @@ moe_status moe_balance_loss_backward(int32_t dtype, int32_t scores, const void *
         if (!seq_offsets && S != 1) return MOE_ERR_INVALID_ARG;
         if (!std::isfinite(coef)) return MOE_ERR_INVALID_ARG;
         if (N == 0) return MOE_OK;
-        if (!given(logits) || !given4(counts) || !given4(seq_weight) || !given(dlogits)) return MOE_ERR_INVALID_ARG;
+        if (!given_rows(logits, dtype, E) || !given4(counts) || !given4(seq_weight) || !given_rows(dlogits, MOE_F32, E))
+            return MOE_ERR_INVALID_ARG;
         if (!aligned4(seq_offsets) || !aligned4(dloss)) return MOE_ERR_INVALID_ARG;
         BalanceArgs a{};
         a.dtype = dtype;

@@ -17,8 +17,9 @@ rank runs the layer for its own N tokens:
      all-to-all whose split sizes are those counts summed per rank);
   3. the received rows arrive ordered (source rank, local expert); they are
      regrouped to (local expert, source rank) with moe_permute_rows so that
-     every local expert has one contiguous slice, and moe_expert_ffn runs
-     the local experts over them;
+     every local expert has one contiguous slice, and moe_expert_ffn (or,
+     on quantised weights, moe_expert_ffn_fp8) runs the local experts over
+     them;
   4. the results go back to the (source rank, local expert) order and to
      their ranks (the reverse all-to-all), and moe_combine weights them in
      token order.  moe_aux_loss gives the rank's Switch loss as in the
@@ -36,8 +37,8 @@ import numpy as np
 import torch
 import torch.distributed as dist
 
-from . import (MoeConfig, make_config, moe_aux_loss, moe_combine, moe_dispatch, moe_expert_ffn, moe_permute_rows,
-               moe_route)
+from . import (MoeConfig, make_config, moe_aux_loss, moe_combine, moe_dispatch, moe_expert_ffn, moe_expert_ffn_fp8,
+               moe_permute_rows, moe_route)
 
 
 class EPPlan(NamedTuple):
@@ -105,7 +106,9 @@ class ExpertParallelMoE:
     cfg: the layer's configuration with this rank's token count N and all E
     experts.  The rank's expert weights follow the layer layout restricted
     to its experts: W1 / W3 [E_r, d_ff, d_model], W2 [E_r, d_model, d_ff],
-    b1 [E_r, d_ff], b2 [E_r, d_model].  ``world`` and ``rank`` default to
+    b1 [E_r, d_ff], b2 [E_r, d_model].  W1, W3 and W2 given as (q, scales)
+    pairs of moe_quantize_weights run as 8-bit experts (bf16 layers only; the
+    rows are exchanged in bf16).  ``world`` and ``rank`` default to
     the process group's; given explicitly (with no group), the phases below
     can be driven by a caller that moves the rows itself.
     """
@@ -149,8 +152,9 @@ class ExpertParallelMoE:
             back = np.empty_like(p.regroup)
             back[p.regroup] = np.arange(rows, dtype=np.int32)
             x_local = moe_permute_rows(x_recv, regroup)
-            y_local = moe_expert_ffn(self.local_config(rows), x_local, torch.from_numpy(p.offsets).to(dev), W1, W2,
-                                     b1=b1, W3=W3, b2=b2)
+            ffn = moe_expert_ffn_fp8 if isinstance(W1, tuple) else moe_expert_ffn
+            y_local = ffn(self.local_config(rows), x_local, torch.from_numpy(p.offsets).to(dev), W1, W2, b1=b1, W3=W3,
+                          b2=b2)
             moe_permute_rows(y_local, torch.from_numpy(back).to(dev), out=y_recv)
         return y_recv
 

@@ -12,6 +12,7 @@ from mixture_experts_layer_53_b200 import build as B
 
 A = ctypes.c_void_p(0x10000)    # never dereferenced
 OFF = ctypes.c_void_p(0x10008)  # not on a 16-byte boundary
+ODD = ctypes.c_void_p(0x10002)  # not on a 4-byte boundary
 WS = ctypes.c_void_p(0x100000)
 BIG = ctypes.c_size_t(1 << 50)
 F = ctypes.c_float
@@ -26,7 +27,7 @@ def lib():
 @pytest.mark.parametrize("args,code", [
     ((2, A, 4, 64, A, A), 1), ((0, A, -1, 64, A, A), 1), ((0, A, 4, 0, A, A), 1), ((0, A, 4, 24, A, A), 2), ((0, A, 4, 2 ** 30 + 16, A, A), 2),
     ((0, A, 2 ** 31, 64, A, A), 2), ((1, None, 4, 64, A, A), 1), ((1, OFF, 4, 64, A, A), 1),
-    ((1, A, 4, 64, None, A), 1), ((1, A, 4, 64, A, OFF), 1), ((1, None, 0, 64, None, None), 0),
+    ((1, A, 4, 64, None, A), 1), ((1, A, 4, 64, A, ODD), 1), ((1, None, 0, 64, None, None), 0),
 ])
 def test_quantize_rows(lib, args, code):
     assert lib.moe_quantize_rows(*args, None) == code
@@ -44,7 +45,7 @@ def test_quantize_weights(lib, args, code):
 
 @pytest.mark.parametrize("change,code", [
     (dict(rows=-1), 1), (dict(n=0), 1), (dict(k=0), 1), (dict(E=0), 1), (dict(E=257), 2), (dict(n=40), 2),
-    (dict(k=40), 2), (dict(rows=2 ** 31), 2), (dict(dt=2), 1), (dict(any=2), 1), (dict(a=None), 1), (dict(a=OFF), 1), (dict(asc=None), 1),
+    (dict(k=40), 2), (dict(rows=2 ** 31), 2), (dict(dt=2), 1), (dict(any=2), 1), (dict(a=None), 1), (dict(a=OFF), 1), (dict(asc=None), 1), (dict(asc=ODD), 1), (dict(wsc=ODD), 1),
     (dict(off=None), 1), (dict(off=ctypes.c_void_p(0x10002)), 1), (dict(n=2 ** 30 + 16), 2), (dict(k=2 ** 30 + 16), 2),
     (dict(w=OFF), 1), (dict(wsc=None), 1), (dict(out=None), 1), (dict(out=OFF), 1),
     (dict(rows=0, a=None, asc=None, out=None), 0),
@@ -66,7 +67,8 @@ def test_ffn(lib):
         assert size(cfg(**bad)) == 0 and call(cfg(**bad), w()) == 2
     assert size(cfg(k=5)) == 0 and call(cfg(k=5), w()) == 1
     for name in ("W1", "W1_scales", "W3", "W3_scales", "W2", "W2_scales"):
-        assert call(cfg(), w(**{name: None})) == 1 and call(cfg(), w(**{name: 0x10008})) == 1
+        bad = 0x10002 if name.endswith("scales") else 0x10008
+        assert call(cfg(), w(**{name: None})) == 1 and call(cfg(), w(**{name: bad})) == 1
     assert call(cfg(), w(b1=0x10000)) == 1                    # a hidden bias with SwiGLU
     assert call(cfg(act="gelu"), w()) == 1                    # W3 with GELU
     assert call(cfg(), w(b2=0x10008)) == 1 and call(cfg(), w(any_scales=-1)) == 1

@@ -249,6 +249,39 @@ def test_captured_step_replayed_on_new_inputs():
         assert all(torch.equal(fwd[k], want[k]) for k in want) and torch.equal(dz, wdz)
 
 
+@pytest.mark.parametrize("E,dtype", [(6, F32), (6, BF), (4, BF), (8, F32), (33, BF)])
+def test_a_part_of_the_tokens(E, dtype):
+    """Logits that start inside a larger tensor, on whatever boundary its rows leave."""
+    z, ids, cuts, mask = inputs(200, E, 2, 1, dtype, E)
+    check(z[37:], ids[37:], np.array([0, 50, 163], np.int32), None, "softmax")
+
+
+def test_on_a_side_stream_with_a_workspace():
+    z, ids, cuts, mask = inputs(5000, 64, 6, 5, F32, 1, padded=True)
+    want, wdz = run(z, ids, cuts, mask, "sigmoid")
+    off, side = torch.from_numpy(cuts).to(DEV), torch.cuda.Stream()
+    ws = torch.empty(1 << 22, dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    got = M.moe_balance_loss(z, ids, seq_offsets=off, token_mask=mask.to(torch.uint8), scores="sigmoid", ws=ws, stream=side)
+    dz = M.moe_balance_loss_backward(z, got, seq_offsets=off, token_mask=mask, scores="sigmoid", stream=side)
+    side.synchronize()
+    assert all(torch.equal(got[k], want[k]) for k in want) and torch.equal(dz, wdz)
+    with pytest.raises(M.MoeError, match="WORKSPACE"):
+        M.moe_balance_loss(z, ids, seq_offsets=off, ws=ws[:1024])
+
+
+def test_the_layers_probabilities_as_logits():
+    """log of moe_route's probabilities are logits of the same softmax scores."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(5)
+    x, Wg = torch.randn((300, 64), generator=g, device=DEV), torch.randn((16, 64), generator=g, device=DEV) * 0.2
+    cfg = M.make_config(300, 64, 64, 16, 4, dtype="f32")
+    ids, _, probs = M.moe_route(cfg, x, Wg, want_probs=True)
+    aux, counts, _ = M.moe_aux_loss(cfg, probs, ids)
+    fwd = M.moe_balance_loss(probs.log(), ids)
+    assert abs(float(fwd["loss"]) - float(aux)) <= REL * float(aux) and torch.equal(fwd["counts"][0], counts)
+
+
 def test_router_gradient_of_a_training_step():
     """The loss from the layer's own routing, its gradient carried to W_g and x by torch: differences in 64 bits."""
     g = torch.Generator(device=DEV)

@@ -431,6 +431,51 @@ def test_layer_on_quantised_experts(N, E, k, act, router):
     assert 1e-4 < rel < 0.1, rel
 
 
+@pytest.mark.parametrize("act", ["swiglu", "gelu"])
+def test_expert_parallel_phase_on_quantised_experts(act):
+    """Two ranks' experts, driven phase by phase as one process: each rank's share on 8-bit weights is the layer's."""
+    from mixture_experts_layer_53_b200 import ep as EP
+    N, d, F, E, k, world = 150, 144, 272, 6, 2, 2
+    _, q = _weights(E, d, F, act, 13, True)
+    g = gen(14)
+    cfg = M.make_config(N, d, F, E, k, act=act, dtype="bf16")
+    x, Wg = torch.randn((N, d), generator=g, device=DEV).to(BF), torch.randn((E, d), generator=g, device=DEV).mul_(0.1).to(BF)
+    ranks = [EP.ExpertParallelMoE(cfg, world=world, rank=r) for r in range(world)]
+    st = ranks[0].dispatch_phase(x, Wg)
+    counts, E_r = st.counts.cpu().numpy(), E // world
+    off = torch.from_numpy(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)).to(DEV)
+    want = M.moe_expert_ffn_fp8(cfg, st.x_sorted, off, q["W1"], q["W2"], W3=q["W3"], b1=q["b1"], b2=q["b2"])
+    back = []
+    for r in range(world):
+        mine = slice(r * E_r, (r + 1) * E_r)
+        # this rank receives rank 0's rows only: its own, or none of another's
+        recv = np.zeros((world, E_r), np.int64)
+        recv[0] = counts[mine]
+        p = EP.plan(counts, recv, world)
+        rows = st.x_sorted[int(counts[:r * E_r].sum()):int(counts[:(r + 1) * E_r].sum())]
+        part = lambda v: None if v is None else (tuple(t[mine].contiguous() for t in v) if isinstance(v, tuple)  # noqa: E731
+                                                 else v[mine].contiguous())
+        back.append(ranks[r].expert_phase(rows, p, part(q["W1"]), part(q["W2"]), W3=part(q["W3"]), b1=part(q["b1"]),
+                                          b2=part(q["b2"])))
+    y_sorted = torch.cat(back)
+    assert torch.equal(y_sorted, want)
+    y, _ = ranks[0].combine_phase(st, y_sorted)
+    assert torch.equal(y, M.moe_combine(cfg, want, st.w, st.inv_perm))
+
+
+def test_workspaces_that_are_too_small_are_refused():
+    _, q = _weights(2, 64, 64, "swiglu", 1, False)
+    cfg = M.make_config(8, 64, 64, 2, 1, act="swiglu", dtype="bf16")
+    x, off, ws = torch.zeros((8, 64), dtype=BF, device=DEV), offsets_of([4, 4]), M.moe_expert_ffn_fp8_workspace(cfg)
+    call = lambda w: M.moe_expert_ffn_fp8(cfg, x, off, q["W1"], q["W2"], W3=q["W3"], ws=w)  # noqa: E731
+    assert not call(ws).any()
+    for bad in (ws[:-1], ws[64:]):
+        with pytest.raises(M.MoeError, match="WORKSPACE"):
+            call(bad)
+    with pytest.raises(ValueError, match="ws"):
+        call(ws.cpu())
+
+
 def test_a_side_stream_owns_its_results():
     """A call given a stream allocates there: its temporaries are not handed to the current stream while it runs."""
     a, w, off = _operands([300, 200], 528, 640, seed=2)
