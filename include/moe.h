@@ -490,7 +490,9 @@ MOE_API moe_status moe_quantize_weights(int32_t dtype, const void *W, int32_t E,
  * below a partial sum's last one: 8e-6 of the result for 14336 terms of one
  * sign, 1e-6 for terms of either; any_scales = 1, which sums blocks of 128
  * outside it, 1.6e-7).  offsets [E+1] is read on the device
- * and held inside 0 .. rows; rows outside every slice are left as they were.
+ * and held inside 0 .. rows, and a slice begins no earlier than the end of
+ * those before it (where offsets decrease, slices are empty or shorter); rows
+ * outside every slice are left as they were.
  * E <= 256.  dev_status (may be NULL): MOE_ERR_TIMEOUT, MOE_ERR_INVALID_ARG
  * (scales, above).  No workspace.
  */

@@ -60,8 +60,10 @@ inline GemmArgs gemm_args(const Fp8GemmArgs &a, int tile_n)
     return g;
 }
 
-// Slices of the rows, held inside 0 .. rows whatever `offsets` says, and the
-// prefix of their m-tile counts.
+// Slices of the rows and the prefix of their m-tile counts.  Whatever
+// `offsets` says, the slices lie inside 0 .. rows and none begins before the
+// end of an earlier one, so that there are never more tiles than the launch
+// allows for (a cluster that shares a tile takes one, and waits for its CTAs).
 struct Slices {
     int warp_sum[kMaxE / 32];
     int off[kMaxE];
@@ -74,6 +76,7 @@ template <int TILE_M> __device__ __forceinline__ void load_slices(Slices *c, con
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int tiles = 0;
+    bool falls = false;
     if (threadIdx.x < kMaxE) {
         const int e = threadIdx.x;
         if (e < g.E) {
@@ -81,6 +84,7 @@ template <int TILE_M> __device__ __forceinline__ void load_slices(Slices *c, con
             c->off[e] = static_cast<int>(lo);
             c->end[e] = static_cast<int>(hi);
             tiles = static_cast<int>((hi - lo + TILE_M - 1) / TILE_M);
+            falls = g.offsets[e + 1] < g.offsets[e];
         }
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -90,7 +94,19 @@ template <int TILE_M> __device__ __forceinline__ void load_slices(Slices *c, con
         if (lane == 31) c->warp_sum[warp] = tiles;
         if (e == 0) c->mt[0] = 0;
     }
-    __syncthreads();
+    if (__syncthreads_or(falls)) {  // offsets that decrease somewhere
+        if (threadIdx.x == 0) {
+            int end = 0, sum = 0;
+            for (int e = 0; e < g.E; ++e) {
+                c->off[e] = end = max(end, c->off[e]);
+                c->end[e] = end = max(end, c->end[e]);
+                sum += static_cast<int>((static_cast<unsigned>(end - c->off[e]) + TILE_M - 1) / TILE_M);
+                c->mt[e + 1] = sum;
+            }
+        }
+        __syncthreads();
+        return;
+    }
     if (threadIdx.x < kMaxE) {
         for (int w = 0; w < warp; ++w) tiles += c->warp_sum[w];
         c->mt[threadIdx.x + 1] = tiles;

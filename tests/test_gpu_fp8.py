@@ -221,6 +221,20 @@ def test_offsets_are_held_inside_the_rows():
     assert (y == 3).all()
 
 
+# (rows, experts, offsets' period): few rows, whose tiles clusters share, with more slices on paper than rows; many
+@pytest.mark.parametrize("rows, E, ups", [(2, 256, (0, 2)), (128, 8, (0, 128)), (9, 24, (3, 9, 1, 5)), (900, 12, (900, 100, 500))])
+@pytest.mark.parametrize("free_scales", [False, True])
+def test_offsets_that_decrease_make_no_row_twice(rows, E, ups, free_scales):
+    """A slice begins no earlier than the end of those before it."""
+    n, k = 144, 2192
+    a, w, _ = _operands([rows] + [0] * (E - 1), n, k, seed=6, free_scales=free_scales)
+    wild = torch.tensor([ups[i % len(ups)] for i in range(E + 1)], dtype=torch.int32, device=DEV)
+    held = torch.cummax(wild, 0).values.to(torch.int32)
+    got, want = (M.moe_expert_matmul_fp8(a, o, w, out=torch.full((rows, n), 5.0, dtype=F32, device=DEV),
+                                         out_dtype=F32, any_scales=free_scales) for o in (wild, held))
+    assert torch.equal(got, want)
+
+
 def test_no_rows_and_empty_slices():
     a, w, off = _operands([0, 0, 0], 64, 64, seed=5)
     assert M.moe_expert_matmul_fp8(a, off, w).shape == (0, 64)
