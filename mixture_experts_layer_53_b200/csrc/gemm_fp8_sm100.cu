@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         bool ok = true;
         for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
             const Tile ti = decode_tile(t, &ctl->slices, g.E, g.n_tiles);
-            const int64_t row_first = ctl->slices.off[ti.e] + ti.m_tile * BM + quarter * 32;
+            const int64_t row_first = static_cast<int64_t>(ctl->slices.off[ti.e]) + ti.m_tile * BM + quarter * 32;
             const int64_t row_end = ctl->slices.end[ti.e];
             const int64_t row = row_first + lane;
             const bool active = row_first < row_end;  // of the whole warp

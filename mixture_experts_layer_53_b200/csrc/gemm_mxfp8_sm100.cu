@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     };
     auto rows_of = [&](const Tile &ti) {
         const int rows = sl->end[ti.e] - sl->off[ti.e], tiles_e = sl->mt[ti.e + 1] - sl->mt[ti.e];
-        const int size = ((rows + tiles_e - 1) / tiles_e + 15) & ~15;
+        const int size = ((rows - 1) / tiles_e + 16) & ~15;
         return Rows{sl->off[ti.e] + ti.m_tile * size, min(size, rows - ti.m_tile * size)};
     };
 

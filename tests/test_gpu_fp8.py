@@ -276,6 +276,27 @@ def test_input_gradient(lengths, n, k):
     assert abs((dyv * np64(pv)).sum() - (np64(dx) * vv).sum()) <= (np.abs(dyv) * pbound).sum() + (bound * np.abs(vv)).sum()
 
 
+@pytest.mark.parametrize("free_scales", [False, True])
+def test_most_rows(free_scales):
+    """The largest number of rows that is taken, in one slice: 2^31 - 1."""
+    rows, n, k, seen = 2 ** 31 - 1, 16, 16, 500
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 120 * 2 ** 30:
+        pytest.skip("needs 120 GiB")
+    a, w, off = _operands([seen], n, k, seed=8, free_scales=free_scales)
+    want = M.moe_expert_matmul_fp8(a, off, w, any_scales=free_scales)
+    q = torch.zeros((rows, k), dtype=a[0].dtype, device=DEV)
+    scales = torch.ones((1, rows), dtype=F32, device=DEV)
+    for part in (slice(0, seen), slice(rows - seen, rows)):
+        q[part], scales[:, part] = a[0], a[1]
+    out = torch.full((rows, n), 7.0, dtype=BF, device=DEV)
+    M.moe_expert_matmul_fp8((q, scales), offsets_of([rows]), w, out=out, any_scales=free_scales)
+    assert torch.equal(out[:seen], want) and torch.equal(out[-seen:], want)
+    assert not any(p.any() for p in out[seen:-seen].split(2 ** 26))
+    del q, scales, out
+    torch.cuda.empty_cache()
+
+
 def test_offsets_beyond_32_bits():
     """Operands and results of more than 2^31 values: the last rows and experts are where they belong."""
     rows, cols = 300_000, 7168
