@@ -36,9 +36,19 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kForwardUnroll = 2, kBackwardUnroll = 1;
 constexpr int kMinChunk = 32;
 constexpr int kMaxChunks = 592;  // 148 SMs x 4 CTAs: one wave
+// Scores of one expert that a lane adds in fp32, one after another, before
+// the sum goes on to fp64; more tokens (from 450,000 of over 64 experts on)
+// take more waves of chunks.  Equal scores round the same way, so a run's
+// error can grow with its length: 1700 additions (8M tokens of 100 experts)
+// were 2e-5 off.
+constexpr int kMaxRun = 96;
 constexpr int kBadId = 1, kBadCut = 2;  // flags of a segment or sequence
 
 __host__ __device__ __forceinline__ int64_t align256(int64_t b) { return (b + 255) & ~static_cast<int64_t>(255); }
+
+// Lanes that hold a token's E scores, and vectors of four experts per lane.
+constexpr int lanes_of(int E) { return E <= 4 ? 1 : E <= 8 ? 2 : E <= 16 ? 4 : E <= 32 ? 8 : E <= 64 ? 16 : 32; }
+constexpr int vectors_of(int E) { return E <= 128 ? 1 : 2; }
 
 // Tokens [chunk c * C, (c + 1) * C) may touch several sequences.  The pairs
 // (c, s) with common tokens increase in both, so c + s numbers them.
@@ -50,7 +60,9 @@ struct Plan {
 Plan make_plan(int64_t N, int E, int S)
 {
     Plan p{};
-    const int64_t even = (N + kMaxChunks - 1) / kMaxChunks;
+    const int64_t most = kMaxRun * (kThreads / lanes_of(E));
+    const int64_t ctas = kMaxChunks * max64(1, (N + kMaxChunks * most - 1) / (kMaxChunks * most));
+    const int64_t even = (N + ctas - 1) / ctas;
     p.chunk = max64(kMinChunk, (even + 15) / 16 * 16);
     p.chunks = max64(1, (N + p.chunk - 1) / p.chunk);
     p.slots = p.chunks + S;
@@ -598,20 +610,24 @@ __global__ void __launch_bounds__(kThreads, 4) balance_backward_kernel(const Bal
 }
 
 // Calls f with the lanes per token and the vectors per lane for E experts.
-template <typename T, bool SIGMOID, typename F> cudaError_t by_width(int E, F &&f)
+template <int W, typename F> cudaError_t of_width(F &&f)
 {
-    if (E <= 4) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
-    if (E <= 8) return f(std::integral_constant<int, 2>{}, std::integral_constant<int, 1>{});
-    if (E <= 16) return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
-    if (E <= 32) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
-    if (E <= 64) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
-    if (E <= 128) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 1>{});
-    return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 2>{});
+    return f(std::integral_constant<int, lanes_of(W)>{}, std::integral_constant<int, vectors_of(W)>{});
+}
+template <typename F> cudaError_t by_width(int E, F &&f)
+{
+    if (E <= 4) return of_width<4>(f);
+    if (E <= 8) return of_width<8>(f);
+    if (E <= 16) return of_width<16>(f);
+    if (E <= 32) return of_width<32>(f);
+    if (E <= 64) return of_width<64>(f);
+    if (E <= 128) return of_width<128>(f);
+    return of_width<kMaxE>(f);
 }
 
 template <typename T, bool SIGMOID> cudaError_t forward(const BalanceArgs &a, const Plan &p, cudaStream_t s)
 {
-    return by_width<T, SIGMOID>(a.E, [&](auto g, auto nv) {
+    return by_width(a.E, [&](auto g, auto nv) {
         return launch_k(balance_partial_kernel<T, decltype(g)::value, decltype(nv)::value, SIGMOID>,
                         dim3(static_cast<unsigned>(p.chunks)), dim3(kThreads), 0, s, a, p);
     });
@@ -620,7 +636,7 @@ template <typename T, bool SIGMOID> cudaError_t forward(const BalanceArgs &a, co
 template <typename T, bool SIGMOID>
 cudaError_t backward(const BalanceArgs &a, int64_t ctas, int64_t per_cta, cudaStream_t s)
 {
-    return by_width<T, SIGMOID>(a.E, [&](auto g, auto nv) {
+    return by_width(a.E, [&](auto g, auto nv) {
         return launch_k(balance_backward_kernel<T, decltype(g)::value, decltype(nv)::value, SIGMOID>,
                         dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, s, a, per_cta);
     });

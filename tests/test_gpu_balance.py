@@ -114,6 +114,19 @@ def test_lengths(N, S, padded):
     check(*inputs(N, 8, 2, S, F32, N + S, padded), "sigmoid")
 
 
+@pytest.mark.parametrize("E,k", [(100, 4), (33, 3), (200, 8), (7, 2)])
+def test_millions_of_tokens_with_equal_scores(E, k):
+    """Equal scores round the same way at every addition: runs of fp32 additions stay short however many tokens there are.
+    Bound as for any length: REL, which has room for fewer than 128 roundings."""
+    N = 8_000_000
+    z = torch.zeros((N, E), device=DEV)
+    ids = (torch.arange(N * k, device=DEV) % E).view(N, k).to(torch.int32)
+    for kind in ("softmax", "sigmoid"):
+        fwd = M.moe_balance_loss(z, ids, scores=kind)
+        assert int(fwd["counts"].sum()) == N * k and int(fwd["status"]) == 0
+        assert abs(float(fwd["loss"]) - k) <= REL * k, float(fwd["loss"])   # sum_e cnt_e / N * E / E = k
+
+
 def test_no_tokens():
     for N, cuts, mask in ((0, [0, 0, 0], None), (9, [0, 0, 9], torch.zeros(9, dtype=torch.bool, device=DEV))):
         z, ids = torch.randn((N, 8), device=DEV), torch.zeros((N, 2), dtype=torch.int32, device=DEV)
