@@ -456,7 +456,8 @@ MOE_API moe_status moe_permute_rows(int32_t dtype, const void *src, const int32_
  * products apply powers of two (or NaN) inside the tensor core; any_scales =
  * 1 takes every fp32 scale (a checkpoint's, for instance) and applies it on
  * the CUDA cores, which costs up to twice the time where the product is
- * bound by arithmetic.  With any_scales = 0 a scale that is no positive normal
+ * bound by arithmetic (blocks whose two scales have a product outside fp32's
+ * normal range are right too, at 300 times the time).  With any_scales = 0 a scale that is no positive normal
  * power of two is taken for the one below it and sets MOE_ERR_INVALID_ARG in
  * dev_status.
  * Layouts, row-major and contiguous:

@@ -28,6 +28,7 @@ constexpr int CHUNK_BYTES = 32 * 64;  // a warp's staging: 32 rows of 64 bytes
 
 struct GemmArgs {
     const int32_t *offsets;
+    const uint8_t *a, *w, *w3;  // [rows, K], [E, n_out, K], [E, n_out, K] (SwiGLU)
     const float *a_scales;   // [kblocks, rows]
     const float *w_scales;   // [E, nblocks, kblocks]
     const float *w3_scales;  // SwiGLU
@@ -44,6 +45,9 @@ inline GemmArgs gemm_args(const Fp8GemmArgs &a, int tile_n)
 {
     GemmArgs g{};
     g.offsets = a.offsets;
+    g.a = static_cast<const uint8_t *>(a.a);
+    g.w = static_cast<const uint8_t *>(a.w);
+    g.w3 = static_cast<const uint8_t *>(a.w3);
     g.a_scales = a.a_scales;
     g.w_scales = a.w_scales;
     g.w3_scales = a.w3_scales;

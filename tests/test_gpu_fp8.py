@@ -192,6 +192,44 @@ def test_scales_of_many_sizes():
         checked(M.moe_expert_matmul_fp8(a, off, w, out_dtype=F32, any_scales=free), want, bound)
 
 
+# (power of two of a's scales, of w's; q's values of a in units of 2^-9, or None: as quantised)
+BEYOND = {"underflow": (-112, -10, None), "far_underflow": (-112, -18, None), "overflow": (80, 50, 3), "zero_blocks": (100, 60, 0)}
+
+
+@pytest.mark.parametrize("name", sorted(BEYOND))
+@pytest.mark.parametrize("free_scales", [False, True])
+def test_scales_whose_product_leaves_fp32(name, free_scales):
+    """Two scales' product below fp32's normal numbers or above its largest, the result inside: the result counts."""
+    ea, ew, small = BEYOND[name]
+    a, w, off = _operands([70, 0, 200], 272, 400, seed=31, free_scales=free_scales)
+    if small is not None:  # few bits, far below the scale: the sum of a block times its scales is finite
+        q = torch.randint(-small, small + 1, a[0].shape, generator=gen(4), device=DEV).float() * 2.0 ** -9
+        a = q.to(E4), torch.ones_like(a[1]) * (1.37 if free_scales else 1.0)
+        v = torch.randint(-3, 4, w[0].shape, generator=gen(5), device=DEV).float() * 2.0 ** -9
+        w = v.to(E4), torch.ones_like(w[1]) * (1.71 if free_scales else 1.0)
+    a, w = (a[0], a[1] * 2.0 ** ea), (w[0], w[1] * 2.0 ** ew)
+    if small is not None:
+        big = a[1].min().double() * w[1].min().double()
+        assert big > torch.finfo(F32).max
+    else:
+        assert float(a[1].max().double() * w[1].max().double()) < torch.finfo(F32).tiny
+    want, bound = R.product(*_values(a, w), off.cpu().numpy())
+    assert np.abs(want).max() < torch.finfo(F32).max
+    y = M.moe_expert_matmul_fp8(a, off, w, out_dtype=F32, any_scales=free_scales)
+    checked(y, want, bound + 2.0 ** -149 * (128 + 8))  # a step of fp32's subnormal numbers for each addition
+
+
+def test_a_block_scale_of_zero_is_a_block_of_zeros():
+    """A checkpoint may hold 0 as the scale of a block without values; beside a large scale it stays 0."""
+    a, w, off = _operands([40, 100], 272, 400, seed=33, free_scales=True)
+    a = a[0], a[1] * 2.0 ** 60
+    a[0].view(torch.uint8)[7] = 0
+    a[1][:, 7] = 2.0 ** -126   # a row of zeros, as the quantiser leaves it
+    w[1][:, 1, 2] = 0.0
+    want, bound = R.product(*_values(a, w), off.cpu().numpy())
+    checked(M.moe_expert_matmul_fp8(a, off, w, out_dtype=F32, any_scales=True), want, bound)
+
+
 def test_scales_that_are_no_powers_of_two_are_reported():
     a, w, off = _operands([20, 30], 64, 272, seed=5)
     for scales, at in ((a[1], (1, 45)), (w[1], (1, 0, 2))):
@@ -389,6 +427,27 @@ def test_ffn(name):
     assert int(status) == 0
     again = M.moe_expert_ffn_fp8(cfg, x, off, q["W1"], q["W2"], b1=q["b1"], W3=q["W3"], b2=q["b2"])
     assert torch.equal(y, again)
+
+
+@pytest.mark.parametrize("act", ["swiglu", "gelu"])
+def test_ffn_scales_whose_product_leaves_fp32(act):
+    """The same inside an FFN: tiny rows (one of zeros) against small weight scales, brought back by large ones."""
+    _, q = _weights(3, 400, 272, act, 8, False)
+    g = gen(9)
+    free = lambda w, e: (w[0], w[1] * torch.exp2(e + torch.rand(w[1].shape, generator=g, device=DEV)))  # noqa: E731
+    off = offsets_of([40, 0, 150])
+    x = (torch.randn((190, 400), generator=gen(4), device=DEV) * 2.0 ** -108).to(BF)
+    x[3] = 0
+    # gate: 2^-115 x 2^-24 = 2^-139 a block, about 2^-119 in all; swiglu's up: 2^-115 x 2^104
+    q["W1"] = free(q["W1"], -13.0)
+    if act == "swiglu":
+        q["W3"] = free(q["W3"], 115.0)
+    q["W2"] = free(q["W2"], 100.0)
+    cfg = M.make_config(190, 400, 272, 3, 1, act=act, dtype="bf16")
+    y = M.moe_expert_ffn_fp8(cfg, x, off, q["W1"], q["W2"], W3=q["W3"], any_scales=True)
+    want, bound = _ffn_reference(q, x, off, act)
+    checked(y, want, bound)
+    assert not y[3].any() and np.sqrt(np.mean(want ** 2)) > 2.0 ** -40
 
 
 @pytest.mark.parametrize("act", ["swiglu", "gelu"])
