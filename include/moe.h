@@ -457,9 +457,10 @@ MOE_API moe_status moe_permute_rows(int32_t dtype, const void *src, const int32_
  * 1 takes every fp32 scale (a checkpoint's, for instance) and applies it on
  * the CUDA cores, which costs up to twice the time where the product is
  * bound by arithmetic (blocks whose two scales have a product outside fp32's
- * normal range are right too, at 300 times the time).  With any_scales = 0 a scale that is no positive normal
- * power of two is taken for the one below it and sets MOE_ERR_INVALID_ARG in
- * dev_status.
+ * normal range are right too, at 300 times the time).  With any_scales = 0 a
+ * scale that is neither a positive normal power of two nor NaN (zero, negative,
+ * subnormal, infinite, any other number) makes the results that it enters NaN
+ * and sets MOE_ERR_INVALID_ARG in dev_status.
  * Layouts, row-major and contiguous:
  *   activations  q [rows, cols] e4m3,    scales [ceil(cols/128), rows] f32
  *   weights      q [E, rows, cols] e4m3, scales [E, ceil(rows/128), ceil(cols/128)] f32

@@ -527,7 +527,7 @@ def moe_expert_matmul_fp8(a: Tuple[torch.Tensor, torch.Tensor], offsets: torch.T
     """Rows offsets[e] .. offsets[e+1]-1 of a times w[e]^T -> [rows, n] (bf16 or f32).
 
     a = (q [rows, k], scales) from moe_quantize_rows, w = (q [E, n, k], scales) from moe_quantize_weights.
-    Scales are powers of two (others set status to 1); any_scales=True takes every fp32 scale, more slowly.
+    Scales are powers of two (others give NaN and set status to 1); any_scales=True takes every fp32 scale, more slowly.
     Rows outside every slice keep what ``out`` held."""
     where = "moe_expert_matmul_fp8"
     (aq, asc), (wq, wsc) = a, w

@@ -5,8 +5,8 @@
 // For row r of expert e (rows offsets[e] .. offsets[e+1]-1):
 //   y[r, c] = sum_kb sA[kb, r] sW[e, c / 128, kb] sum_{k in kb} a[r, k] w[e, c, k]
 // A power of two is its exponent, and a fp32 scale's exponent field is the
-// hardware's UE8M0 code (255 for NaN), so the fp32 scale tensors are read as
-// they are.  The whole reduction accumulates in TMEM in fp32; nothing is
+// hardware's UE8M0 code (255, NaN, for what is no such power), so the fp32
+// scale tensors are read as they are.  The whole reduction accumulates in TMEM in fp32; nothing is
 // added on the CUDA cores (gemm_fp8_sm100.cu, for other scales, does that and
 // spends more time on it than the tensor core on the products).
 //
@@ -471,12 +471,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                     t_ahead += step;
                 }
             };
-            // exponent codes; a scale that is no power of two and no NaN
-            // (zero, negative, infinite, any mantissa) is reported
+            // exponent codes; a scale that is neither a positive normal power
+            // of two nor NaN is reported, and its products are NaN: whoever
+            // does not look at the status sees it too
             auto code = [&](float v) {
                 const uint32_t b = __float_as_uint(v), e = b >> 23;
-                odd_scale |= e == 0 || e > 255 || (e < 255) == ((b & 0x7FFFFFu) != 0);
-                return e & 255u;
+                const bool nan = (b & 0x7FFFFFFFu) > 0x7F800000u, pow2 = e - 1u < 254u && (b & 0x7FFFFFu) == 0;
+                odd_scale |= !nan && !pow2;
+                return pow2 ? e : 255u;
             };
             for (int i = 0; i + 1 < AHEAD; ++i) fetch(ctl->ahead[atom][i]);
             uint32_t group = 0;

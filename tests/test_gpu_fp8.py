@@ -249,6 +249,40 @@ def test_scales_that_are_no_powers_of_two_are_reported():
     assert int(status) == 0
 
 
+@pytest.mark.parametrize("lengths,n,k", [([20, 30], 272, 272), ([200, 9, 330], 400, 272), ([3], 160, 8208)])
+@pytest.mark.parametrize("bad", [1.5, 0.0, -1.0, 1e-40, float("inf"), -float("inf")])
+def test_a_scale_that_is_no_power_of_two_shows_in_the_results(lengths, n, k, bad):
+    """Without a status word too: the results that the scale enters are NaN, all others as they were."""
+    a, w, off = _operands(lengths, n, k, seed=7)
+    clean = M.moe_expert_matmul_fp8(a, off, w, out_dtype=F32)
+    hit = torch.zeros_like(clean, dtype=torch.bool)
+    keep = float(a[1][1, 1])
+    a[1][1, 1] = bad
+    hit[1] = True
+    y = M.moe_expert_matmul_fp8(a, off, w, out_dtype=F32)
+    assert torch.isnan(y[hit]).all() and torch.equal(y[~hit], clean[~hit])
+    a[1][1, 1] = keep
+    w[1][0, 1, 2] = bad                                    # columns 128 .. 255 of the first expert's rows
+    hit[:] = False
+    hit[:lengths[0], 128:256] = True
+    y = M.moe_expert_matmul_fp8(a, off, w, out_dtype=F32)
+    assert torch.isnan(y[hit]).all() and torch.equal(y[~hit], clean[~hit])
+
+
+def test_a_nan_scale_of_either_sign_is_a_nan():
+    a, w, off = _operands([20, 30], 64, 272, seed=5)
+    clean = M.moe_expert_matmul_fp8(a, off, w)
+    for bits in (0x7FC00000, 0x7F800001, -0x400000, -0x7FFFFF):
+        b = a[1].clone()
+        b.view(torch.int32)[1, 45] = bits
+        assert torch.isnan(b[1, 45])
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        y = M.moe_expert_matmul_fp8((a[0], b), off, w, status=status)
+        assert int(status) == 0 and torch.isnan(y[45]).all()
+        y[45] = clean[45]
+        assert torch.equal(y, clean)
+
+
 def test_offsets_are_held_inside_the_rows():
     a, w, off = _operands([10, 20, 30], 64, 64, seed=4)
     wild = torch.tensor([-5, 10, 30, 10 ** 9], dtype=torch.int32, device=DEV)
