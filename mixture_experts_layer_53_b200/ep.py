@@ -100,6 +100,14 @@ class DispatchState(NamedTuple):
     counts: torch.Tensor    # [E] int32
 
 
+def _quantised(W1, any_scales: bool) -> bool:
+    """Whether expert weights are (q, scales) pairs."""
+    pair = isinstance(W1, (tuple, list))
+    if any_scales and not pair:
+        raise ValueError("any_scales is for (q, scales) weights")
+    return pair
+
+
 class ExpertParallelMoE:
     """One rank's share of an expert-parallel layer (see the module docstring).
 
@@ -108,7 +116,11 @@ class ExpertParallelMoE:
     to its experts: W1 / W3 [E_r, d_ff, d_model], W2 [E_r, d_model, d_ff],
     b1 [E_r, d_ff], b2 [E_r, d_model].  W1, W3 and W2 given as (q, scales)
     pairs of moe_quantize_weights run as 8-bit experts (bf16 layers only; the
-    rows are exchanged in bf16).  ``world`` and ``rank`` default to
+    rows are exchanged in bf16); ``any_scales`` takes pairs whose scales are
+    no powers of two, a checkpoint's for instance, as in moe_expert_ffn_fp8.
+    ``status`` (a zeroed int32 [1] tensor on the rank's device) receives the
+    expert FFN's device status, for weights of either kind.
+    ``world`` and ``rank`` default to
     the process group's; given explicitly (with no group), the phases below
     can be driven by a caller that moves the rows itself.
     """
@@ -140,10 +152,12 @@ class ExpertParallelMoE:
 
     def expert_phase(self, x_recv: torch.Tensor, p: EPPlan, W1: torch.Tensor, W2: torch.Tensor,
                      W3: Optional[torch.Tensor] = None, b1: Optional[torch.Tensor] = None,
-                     b2: Optional[torch.Tensor] = None) -> torch.Tensor:
+                     b2: Optional[torch.Tensor] = None, any_scales: bool = False,
+                     status: Optional[torch.Tensor] = None) -> torch.Tensor:
         """Step 3: the received rows, in (source rank, local expert) order,
         regrouped by local expert, through the local experts and back to the
         received order."""
+        quantised = _quantised(W1, any_scales)
         rows = x_recv.shape[0]
         y_recv = torch.empty_like(x_recv)
         if rows > 0:
@@ -152,9 +166,12 @@ class ExpertParallelMoE:
             back = np.empty_like(p.regroup)
             back[p.regroup] = np.arange(rows, dtype=np.int32)
             x_local = moe_permute_rows(x_recv, regroup)
-            ffn = moe_expert_ffn_fp8 if isinstance(W1, tuple) else moe_expert_ffn
-            y_local = ffn(self.local_config(rows), x_local, torch.from_numpy(p.offsets).to(dev), W1, W2, b1=b1, W3=W3,
-                          b2=b2)
+            cfg, offsets = self.local_config(rows), torch.from_numpy(p.offsets).to(dev)
+            kw = dict(b1=b1, W3=W3, b2=b2, status=status)
+            if quantised:
+                y_local = moe_expert_ffn_fp8(cfg, x_local, offsets, W1, W2, any_scales=any_scales, **kw)
+            else:
+                y_local = moe_expert_ffn(cfg, x_local, offsets, W1, W2, **kw)
             moe_permute_rows(y_local, torch.from_numpy(back).to(dev), out=y_recv)
         return y_recv
 
@@ -166,18 +183,20 @@ class ExpertParallelMoE:
 
     def forward(self, x: torch.Tensor, W_g: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor,
                 W3: Optional[torch.Tensor] = None, b1: Optional[torch.Tensor] = None,
-                b2: Optional[torch.Tensor] = None, b_e: Optional[torch.Tensor] = None):
+                b2: Optional[torch.Tensor] = None, b_e: Optional[torch.Tensor] = None, any_scales: bool = False,
+                status: Optional[torch.Tensor] = None):
         """Returns (y [N, d_model], aux [1] f32: this rank's Switch loss).
 
         b_e (sigmoid router) selects as in moe_forward; its sign-rule step
         is left to the caller (moe_aux_loss with gamma and b_e, on this
         rank's counts or on counts all-reduced over the group)."""
         cfg, world, E_r, g = self.cfg, self.world, self.E_r, self.group
+        _quantised(W1, any_scales)  # refused before anything is exchanged
         st = self.dispatch_phase(x, W_g, b_e)
         recv_counts = exchange(st.counts, [E_r] * world, [E_r] * world, g)
         host = torch.cat([st.counts, recv_counts]).cpu().numpy()
         p = plan(host[:cfg.E], host[cfg.E:].reshape(world, E_r), world)
         x_recv = exchange(st.x_sorted, p.send_rows, p.recv_rows, g)
-        y_recv = self.expert_phase(x_recv, p, W1, W2, W3=W3, b1=b1, b2=b2)
+        y_recv = self.expert_phase(x_recv, p, W1, W2, W3=W3, b1=b1, b2=b2, any_scales=any_scales, status=status)
         y_sorted = exchange(y_recv, p.recv_rows, p.send_rows, g)
         return self.combine_phase(st, y_sorted)

@@ -117,3 +117,54 @@ def test_two_gloo_ranks_expert_parallel():
                            start_method="spawn")
         assert results["rows0"] + results["rows1"] == 37 * 2  # every assignment reached its expert once
         assert results["err0"] < 1e-12 and results["err1"] < 1e-12, dict(results)
+
+
+@pytest.mark.parametrize("kind", [tuple, list, None])
+def test_scales_and_status_reach_the_expert_ffn(monkeypatch, kind):
+    """expert_phase and forward hand any_scales and status on; (q, scales) in a tuple or a list are 8-bit experts."""
+    calls = []
+
+    def ffn(name):
+        def call(cfg, x, offsets, W1, W2, **kw):
+            calls.append((name, W1, W2, kw))
+            return x + 1
+        return call
+
+    def permute(src, dst_row, out=None):
+        out = torch.empty_like(src) if out is None else out
+        out[dst_row.long()] = src
+        return out
+
+    monkeypatch.setattr(EP, "moe_expert_ffn_fp8", ffn("fp8"))
+    monkeypatch.setattr(EP, "moe_expert_ffn", ffn("plain"))
+    monkeypatch.setattr(EP, "moe_permute_rows", permute)
+    cfg = EP.make_config(3, 16, 16, 4, 1, act="swiglu", dtype="bf16")
+    layer = EP.ExpertParallelMoE(cfg, world=2, rank=0)
+    counts = np.array([1, 0, 0, 2])
+    p = EP.plan(counts, np.array([[1, 0], [1, 1]]), 2)
+    x, status = torch.arange(48.0).view(3, 16), torch.zeros(1, dtype=torch.int32)
+    w = torch.zeros(2, 16, 16)
+    W = w if kind is None else kind((w, torch.ones(2, 1, 1)))
+    y = layer.expert_phase(x, p, W, W, W3=W, any_scales=kind is not None, status=status)
+    assert torch.equal(y, x + 1)
+    name, W1, W2, kw = calls[-1]
+    assert W1 is W and W2 is W and kw["W3"] is W and kw["status"] is status
+    assert name == ("plain" if kind is None else "fp8") and kw.get("any_scales") == (True if kind else None)
+    if kind is None:
+        with pytest.raises(ValueError, match="any_scales"):
+            layer.expert_phase(x, p, W, W, W3=W, any_scales=True)
+    # forward passes them to expert_phase
+    seen = {}
+    monkeypatch.setattr(layer, "dispatch_phase", lambda x, W_g, b_e: EP.DispatchState(
+        None, None, None, x, None, torch.from_numpy(counts.astype(np.int32))))
+    monkeypatch.setattr(EP, "exchange", lambda t, *a: t)
+    monkeypatch.setattr(EP, "plan", lambda *a: p)
+    monkeypatch.setattr(layer, "expert_phase", lambda x, p, W1, W2, **kw: seen.update(kw) or x)
+    monkeypatch.setattr(layer, "combine_phase", lambda st, y: (y, None))
+    if kind is None:
+        with pytest.raises(ValueError, match="any_scales"):
+            layer.forward(x, None, W, W, W3=W, any_scales=True, status=status)
+        assert not seen
+        return
+    layer.forward(x, None, W, W, W3=W, any_scales=True, status=status)
+    assert seen["any_scales"] is True and seen["status"] is status

@@ -591,6 +591,31 @@ def test_expert_parallel_phase_on_quantised_experts(act):
     assert torch.equal(y, M.moe_combine(cfg, want, st.w, st.inv_perm))
 
 
+def test_expert_parallel_phase_with_a_checkpoints_scales():
+    """Scales that are no powers of two through the expert-parallel phase: with any_scales the single process's result,
+    without it a status (and NaN); the status of a layer on bf16 weights is wired too."""
+    from mixture_experts_layer_53_b200 import ep as EP
+    N, d, F, E = 70, 144, 272, 3
+    W, q = _weights(E, d, F, "swiglu", 15, False)
+    g = gen(16)
+    free = lambda w: [w[0], w[1] * torch.exp(torch.randn(w[1].shape, generator=g, device=DEV))]  # noqa: E731
+    f = {k: free(q[k]) for k in ("W1", "W2", "W3")}
+    cfg = M.make_config(N, d, F, E, 1, act="swiglu", dtype="bf16")
+    x = torch.randn((N, d), generator=g, device=DEV).to(BF)
+    counts = np.array([20, 0, 50])
+    off = offsets_of(counts)
+    layer, p = EP.ExpertParallelMoE(cfg, world=1, rank=0), EP.plan(counts, counts[None], 1)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    y = layer.expert_phase(x, p, f["W1"], f["W2"], W3=f["W3"], any_scales=True, status=status)
+    assert torch.equal(y, M.moe_expert_ffn_fp8(cfg, x, off, f["W1"], f["W2"], W3=f["W3"], any_scales=True)) and int(status) == 0
+    want, bound = _ffn_reference({**q, **f}, x, off, "swiglu")
+    checked(y, want, bound)
+    y = layer.expert_phase(x, p, f["W1"], f["W2"], W3=f["W3"], status=status)
+    assert int(status) == 1 and torch.isnan(y).all()
+    plain = layer.expert_phase(x, p, W["W1"], W["W2"], W3=W["W3"], status=status.zero_())
+    assert torch.equal(plain, M.moe_expert_ffn(cfg, x, off, W["W1"], W["W2"], W3=W["W3"])) and int(status) == 0
+
+
 def test_workspaces_that_are_too_small_are_refused():
     _, q = _weights(2, 64, 64, "swiglu", 1, False)
     cfg = M.make_config(8, 64, 64, 2, 1, act="swiglu", dtype="bf16")
