@@ -463,6 +463,109 @@ def test_ffn(name):
     assert torch.equal(y, again)
 
 
+# CTAs that process several tiles: what they carry from one to the next (barrier phases, stages, slots of scales, sets of
+# accumulators) shows in results only with more tiles than SMs.
+# name: (rows of an expert, experts, n, k, the tile's rows and columns)
+SEVERAL_TILES = {
+    "wide": ((200, 500), 24, 2000, 656, 240, 256),
+    "tall": ((200, 480), 20, 2000, 656, 240, 128),
+    "few": ((20, 130), 40, 2000, 656, 112, 256),
+    "tiny": ((1, 28), 48, 2000, 656, 32, 256),
+}
+
+
+def _lengths(between, E, seed):
+    """Uneven slices, one of them empty."""
+    lengths = np.random.RandomState(seed).randint(between[0], between[1] + 1, E)
+    lengths[E // 3] = 0
+    return [int(v) for v in lengths]
+
+
+def _several(lengths, n, tile_rows, tile_cols):
+    tiles = sum(-(-v // tile_rows) for v in lengths) * -(-n // tile_cols)
+    assert tiles > 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    assert n % tile_cols
+
+
+@pytest.mark.parametrize("name", sorted(SEVERAL_TILES))
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("free_scales", [False, True])
+def test_product_of_several_tiles_a_cta(name, out, free_scales):
+    between, E, n, k, tile_rows, tile_cols = SEVERAL_TILES[name]
+    lengths = _lengths(between, E, E)
+    _several(lengths, n, *((128, 256) if free_scales else (tile_rows, tile_cols)))
+    a, w, off = _operands(lengths, n, k, seed=E, free_scales=free_scales, behind=5)
+    y = torch.full((sum(lengths) + 5, n), 7.0, dtype=out, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    M.moe_expert_matmul_fp8(a, off, w, out_dtype=out, out=y, any_scales=free_scales, status=status)
+    assert (y[-5:] == 7).all() and int(status) == 0
+    want, bound = R.product(*_values(a, w), off.cpu().numpy())
+    checked(y[:-5], want[:-5], (bound + (R.UBF * (np.abs(want) + bound) if out == BF else 0))[:-5])
+
+
+# name: (rows of an expert, experts, d, F, activation, biases, the first product's tile's rows; its columns are 128)
+SEVERAL_TILES_FFN = {
+    "wide": ((200, 500), 16, 656, 2000, "swiglu", True, 240),
+    "few": ((20, 130), 24, 656, 2000, "swiglu", False, 112),
+    "tiny": ((1, 28), 40, 656, 2000, "swiglu", False, 32),
+    "gelu_tall": ((200, 500), 16, 656, 2000, "gelu", True, 240),
+    "gelu_tiny": ((1, 28), 40, 656, 2000, "gelu", True, 32),
+}
+
+
+@pytest.mark.parametrize("name", sorted(SEVERAL_TILES_FFN))
+def test_ffn_of_several_tiles_a_cta(name):
+    between, E, d, F, act, biases, tile_rows = SEVERAL_TILES_FFN[name]
+    lengths = _lengths(between, E, E)
+    _several(lengths, F, tile_rows, 128)
+    _, q = _weights(E, d, F, act, E, biases)
+    rows, off = sum(lengths), offsets_of(lengths)
+    x = torch.randn((rows, d), generator=gen(4), device=DEV).to(BF)
+    cfg = M.make_config(rows, d, F, E, 1, act=act, dtype="bf16")
+    want, bound = _ffn_reference(q, x, off, act)
+    assert np.sqrt(np.mean(bound ** 2)) < 0.1 * np.sqrt(np.mean(want ** 2))   # as in test_ffn
+    for free in (False, True):
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        y = M.moe_expert_ffn_fp8(cfg, x, off, q["W1"], q["W2"], b1=q["b1"], W3=q["W3"], b2=q["b2"], any_scales=free, status=status)
+        checked(y, want, bound)
+        assert int(status) == 0
+
+
+@pytest.mark.parametrize("tokens", [3, 700])
+@pytest.mark.parametrize("free_scales", [False, True])
+def test_ffn_on_weights_and_slices_written_just_before(tokens, free_scales):
+    """The products of an FFN fetch weights and slices ahead of their rows, never ahead of the kernels that write them:
+    quantisers and copies of some hundred MB straight before the call, on one stream."""
+    E, d, F = 24, 2048, 1408
+    sets = []
+    for seed in (1, 2):
+        W, _ = _weights(E, d, F, "swiglu", seed, False)
+        lengths = np.random.RandomState(seed).multinomial(tokens, np.ones(E) / E)
+        sets.append((W, offsets_of(lengths), torch.randn((tokens, d), generator=gen(seed), device=DEV).to(BF)))
+    cfg = M.make_config(tokens, d, F, E, 1, act="swiglu", dtype="bf16")
+    ffn = lambda q, off, x: M.moe_expert_ffn_fp8(cfg, x, off, q["W1"], q["W2"], W3=q["W3"], any_scales=free_scales)  # noqa: E731
+    names = ("W2", "W3", "W1")   # W1 last: the first product's weights are the newest
+    want, qs = [], []
+    for W, off, x in sets:
+        qs.append({n: M.moe_quantize_weights(W[n]) for n in names})
+        torch.cuda.synchronize()
+        want.append(ffn(qs[-1], off, x))
+        torch.cuda.synchronize()
+    at = {n: (torch.empty_like(qs[0][n][0]), torch.empty_like(qs[0][n][1])) for n in names}
+    off, x, got = torch.empty_like(sets[0][1]), torch.empty_like(sets[0][2]), []
+    for i in range(6):
+        W, o, v = sets[i % 2]
+        got.append(ffn({n: M.moe_quantize_weights(W[n]) for n in names}, o, v))   # quantised just before
+        x.copy_(v)
+        off.copy_(o)
+        for n in names:
+            at[n][1].copy_(qs[i % 2][n][1])
+            at[n][0].view(torch.uint8).copy_(qs[i % 2][n][0].view(torch.uint8))
+        got.append(ffn(at, off, x))                                               # copied just before
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i // 2 % 2]) for i, y in enumerate(got))
+
+
 @pytest.mark.parametrize("act", ["swiglu", "gelu"])
 def test_ffn_scales_whose_product_leaves_fp32(act):
     """The same inside an FFN: tiny rows (one of zeros) against small weight scales, brought back by large ones."""
