@@ -19,13 +19,17 @@ constexpr int kMaxK = 16;
 __host__ __device__ __forceinline__ int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
 __host__ __device__ __forceinline__ int64_t max64(int64_t a, int64_t b) { return a > b ? a : b; }
 
-// Programmatic dependent launch.  Every kernel of this library starts with
-// pdl_enter(): griddepcontrol.wait returns once the previous grid on the
-// stream has completed and its memory is visible (immediately if there is no
-// programmatic dependency), so nothing below it can race with the
-// predecessor; launch_dependents then lets the next kernel's CTAs be
-// scheduled while this grid runs, hiding the launch latency between the
-// kernels of one forward.
+// Programmatic dependent launch.  Every thread of this library's kernels that
+// reads or writes global memory calls pdl_enter() first: griddepcontrol.wait
+// returns once the previous grid on the stream has completed and its memory
+// is visible (immediately if there is no programmatic dependency), so nothing
+// below it can race with the predecessor; launch_dependents then lets the
+// next kernel's CTAs be scheduled while this grid runs, hiding the launch
+// latency between the kernels of one forward.  One exception: an expert
+// product inside moe_expert_ffn_fp8 reads its slices and weights before it
+// (gemm_mxfp8_sm100.cu), because its predecessor is a kernel of the same call
+// that does not write them and has itself waited for whoever did.  So a kernel
+// that is followed by such a product must wait before launch_dependents too.
 __device__ __forceinline__ void pdl_enter()
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");

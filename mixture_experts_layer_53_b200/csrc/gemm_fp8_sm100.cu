@@ -43,13 +43,34 @@ namespace {
 
 using namespace fp8;
 
+constexpr int BM = 128;          // rows of a CTA's tile
+constexpr int BN = 256;          // accumulator columns of a tile
 constexpr int STAGES = 4;
+constexpr int CHUNK_BYTES = 32 * 64;  // a warp's staging: 32 rows of 64 bytes
 constexpr int ROLE_REGS = 56, SUM_REGS = 224;
 static_assert(32 * FIRST_SUM_WARP * ROLE_REGS + 32 * SUM_WARPS * SUM_REGS <= THREADS * LAUNCH_REGS, "register split");
 constexpr int A_BYTES = BM * BK;
 constexpr int W_BYTES = BN * BK;
 constexpr int STAGE_BYTES = A_BYTES + W_BYTES;
 constexpr uint32_t TMEM_COLS = 512;
+
+// The two halves of a row's 128 hidden units (SwiGLU: two warps) exchange
+// their largest |h|.  Two sets of values by phase: a warp that is a tile
+// ahead writes the other set, and it cannot be two ahead.
+struct Exchange {
+    uint32_t amax[2][2][BM];  // [phase][half][row]
+    uint64_t there[4];        // per lane quarter: both halves' values are there (count 2)
+};
+__device__ __forceinline__ bool exchange_amax(Exchange *x, uint32_t &m, uint32_t phase, int quarter, int half, int lane,
+                                              volatile int *abort_flag, int32_t *status)
+{
+    x->amax[phase][half][quarter * 32 + lane] = m;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&x->there[quarter]);
+    if (!__all_sync(0xffffffffu, mbar_wait(&x->there[quarter], phase, abort_flag, status))) return false;
+    m = max(m, x->amax[phase][half ^ 1][quarter * 32 + lane]);
+    return true;
+}
 
 struct Ctl {
     alignas(1024) uint8_t stage[SUM_WARPS][CHUNK_BYTES];
@@ -66,6 +87,80 @@ struct Ctl {
 
 constexpr size_t kSmemBytes = 1024 + STAGES * STAGE_BYTES + sizeof(Ctl);
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+
+template <int EPI> __host__ __device__ constexpr int out_cols() { return EPI == EPI_SWIGLU ? 128 : 256; }
+
+// 32 values of a thread's row from column c on, as e4m3.
+__device__ __forceinline__ void store_h32(const float *h, float inv, uint8_t *row, int c, int n_out)
+{
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        if (c + 16 * p < n_out) {
+            const float *v = h + 16 * p;
+            st16(row + c + 16 * p,
+                 make_uint4(cvt_e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                            cvt_e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv),
+                            cvt_e4m3x4(v[8] * inv, v[9] * inv, v[10] * inv, v[11] * inv),
+                            cvt_e4m3x4(v[12] * inv, v[13] * inv, v[14] * inv, v[15] * inv)));
+        }
+    }
+}
+
+// Eight bias values of columns c .. c+7 (zero past n_out or without bias).
+__device__ __forceinline__ void bias8(const __nv_bfloat16 *bias, int c, int n_out, float (&b)[8])
+{
+    const uint4 v = (bias && c < n_out) ? __ldg(reinterpret_cast<const uint4 *>(bias + c)) : make_uint4(0u, 0u, 0u, 0u);
+    unpack16(v, b, static_cast<const __nv_bfloat16 *>(nullptr));
+}
+
+// Writes the four 16-byte pieces that each lane holds of its own row as
+// 64-byte row segments: through the warp's staging buffer, piece j of row r
+// at j ^ ((r >> 1) & 3) (free of bank conflicts both ways).
+__device__ __forceinline__ void store_chunk(const uint4 (&p)[4], uint8_t *stage, uint8_t *out, int64_t row_bytes,
+                                            int64_t row_first, int64_t row_end, int64_t byte0, int64_t byte_end, int lane)
+{
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) st16(stage + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), p[j]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2), j = lane & 3;
+        const uint4 v = *reinterpret_cast<const uint4 *>(stage + r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
+        if (row_first + r < row_end && byte0 + j * 16 < byte_end)
+            st16(out + (row_first + r) * row_bytes + byte0 + j * 16, v);
+    }
+}
+
+// A chunk of 32 result columns from column col on (v: a thread's row, bias
+// not yet added), as bf16 or fp32 rows.
+template <int EPI>
+__device__ __forceinline__ void store_columns(float (&v)[32], const __nv_bfloat16 *bias, const GemmArgs &g, int col,
+                                              int64_t row_first, int64_t row_end, uint8_t *stage, int lane)
+{
+    constexpr int ES = EPI == EPI_BF16 ? 2 : 4;
+    const int64_t row_bytes = static_cast<int64_t>(g.n_out) * ES;
+    if (bias) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float b[8];
+            bias8(bias, col + 8 * j, g.n_out, b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[8 * j + i] += b[i];
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < ES / 2; ++q) {
+        uint4 p[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (EPI == EPI_BF16) p[j] = pack16(v + 8 * j, static_cast<const __nv_bfloat16 *>(nullptr));
+            else p[j] = pack16(v + 16 * q + 4 * j, static_cast<const float *>(nullptr));
+        }
+        store_chunk(p, stage, static_cast<uint8_t *>(g.out), row_bytes, row_first, row_end,
+                    static_cast<int64_t>(col) * ES + 64 * q, row_bytes, lane);
+    }
+}
 
 // D[tmem] (+)= A[smem] * B[smem]^T, e4m3 inputs, fp32 accumulate.
 __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
