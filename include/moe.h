@@ -456,7 +456,7 @@ MOE_API moe_status moe_permute_rows(int32_t dtype, const void *src, const int32_
  * products apply powers of two (or NaN) inside the tensor core; any_scales =
  * 1 takes every fp32 scale (a checkpoint's, for instance) and applies it on
  * the CUDA cores, which costs up to twice the time where the product is
- * bound by arithmetic (blocks whose two scales have a product outside fp32's
+ * bound by arithmetic and an eighth to a quarter more at few rows (blocks whose two scales have a product outside fp32's
  * normal range are right too, at 300 times the time).  With any_scales = 0 a
  * scale that is neither a positive normal power of two nor NaN (zero, negative,
  * subnormal, infinite, any other number) makes the results that it enters NaN

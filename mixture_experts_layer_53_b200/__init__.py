@@ -620,8 +620,8 @@ def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, seq_offsets: 
     """Balance loss over sequences from router logits [N, E] (f32 or bf16) and topk_ids [N, k] int32.
 
     seq_offsets [S + 1] int32 (default: one sequence), token_mask [N] bool or uint8 (False: padding), scores
-    "softmax" or "sigmoid" (normalised).  moe_route's probabilities serve as softmax logits by their logarithm, with a
-    softmax router for the gradient too.  Returns loss [1], counts [S, E] int32, seq_weight [S] (for the gradient) and
+    "softmax" or "sigmoid" (normalised).  moe_route's probabilities, softmax(z) for every router, serve as logits of
+    softmax scores by their logarithm.  Returns loss [1], counts [S, E] int32, seq_weight [S] (for the gradient) and
     status [1] int32 (6: an expert id out of range, 1: bad seq_offsets)."""
     where, dev = "moe_balance_loss", logits.device
     N, E, S, off, mask = _sequences(where, logits, seq_offsets, token_mask)

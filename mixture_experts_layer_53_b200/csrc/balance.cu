@@ -16,7 +16,8 @@
 // (and writing the gradient); the exponentials run on the special-function
 // unit.  Everything is summed in a fixed order (floats) or in integers: equal
 // inputs give equal bits.  131072 tokens x 256 experts of fp32, sigmoid scores:
-// the loss 42 us (two kernels; reading takes 21), the gradient 46 us (41).
+// the loss's two kernels 37 and 14 us (reading takes 21), the gradient 48 us (41);
+// the step, whose kernels' starts and ends overlap, 86 us.
 #include <cuda_runtime.h>
 
 #include <type_traits>

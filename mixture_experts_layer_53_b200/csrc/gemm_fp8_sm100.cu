@@ -12,8 +12,9 @@
 // It takes any scales; powers of two are faster left to the tensor core
 // (gemm_mxfp8_sm100.cu).  What bounds it is the epilogue warps: reading and
 // adding a k-block's accumulator takes them longer than the MMA's 512 cycles
-// (Mixtral's FFN, 4096 tokens: 1.94 ms, and 1.25 ms with powers of two;
-// DeepSeek-V3's 3.5 and 2.2 ms).
+// (short runs: Mixtral's FFN, 4096 tokens: 2.2-2.4 ms, and 1.25-1.45 ms with
+// powers of two; DeepSeek-V3's 3.7-4.1 and 2.1-2.2 ms).  Few rows: 32 rows of 8
+// experts, n = 4096, k = 14336: 91 us and 80; one token of DeepSeek-V3: 93 and 73.
 //
 // Warp roles (384 threads, one CTA per SM, persistent over the tile list
 // (expert, n-tile, m-tile), m-tiles innermost so that CTAs that run at the

@@ -39,7 +39,8 @@
 // Measured (events, short runs; 6.55 TB/s is this card's copy rate): 8 experts
 // x 1024 rows, n = 8192, k = 4096: 234 us, 2.34 PFLOP/s (under the power cap,
 // looped: 2.1); 512 tokens of DeepSeek-V3's FFN: 1.69 ms, 6.7 TB/s; 32 rows, n =
-// 4096, k = 14336: 75 us, 6.2 TB/s; 131072 rows, n = 2048, k = 768, fp32: 303 us.
+// 4096, k = 14336: 75 us, 6.2 TB/s; 131072 rows, n = 2048, k = 768, fp32: 303 us
+// (370 in a loop).
 //
 // Warp roles (384 threads, one CTA per SM, persistent):
 //   warp 0      TMA producer: per k-block of 128 values W (16 KB for each

@@ -4,8 +4,9 @@
 // Both kernels read every value once, keep it in registers while the block's
 // max |x| is formed, and write one byte per value: they are bound by HBM
 // (3 bytes per bf16 value, 5 per fp32 value, plus the scales).  Measured:
-// 32768 x 7168 bf16 rows in 111 us (6.4 TB/s), 8 x 14336 x 4096 bf16 weights,
-// transposed, in 221 us (6.4 TB/s); a copy reaches 6.55.
+// 32768 x 7168 bf16 rows in 115 us (6.2 TB/s), 8 x 14336 x 4096 bf16 weights,
+// transposed, in 231 us (6.1 TB/s), calls with changing inputs; a copy reaches
+// 6.55.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
