@@ -189,13 +189,16 @@ template <int EPI> __device__ __forceinline__ uint32_t chunk_col(int c, int half
     return EPI == EPI_SWIGLU ? (c >> 1) * 128 + half * 64 + (c & 1) * 32 : half * 128 + c * 32;
 }
 
-// Whether the fp32 product of two scales is too small or too large for its
-// block's sums (zero, or 2^-18 to 2^25 in size): subnormal or zero, so that
-// bits are lost, or infinite, which times zero is no number.
-__device__ __forceinline__ bool beyond_f32(float p)
+__device__ __forceinline__ bool not_normal(float p) { return (__float_as_uint(p) & 0x7FFFFFFFu) - 0x00800000u >= 0x7F000000u; }
+
+// Whether p, the fp32 product of the scales a and b, is too small or too large
+// for a block's sums (zero, or 2^-18 to 2^25 in size): subnormal or zero, so
+// that bits are lost, or infinite of finite scales, which times zero is no
+// number.
+__device__ __forceinline__ bool beyond_f32(float p, float a, float b)
 {
-    const uint32_t b = __float_as_uint(p) & 0x7FFFFFFFu;
-    return b < 0x00800000u || b == 0x7F800000u;
+    const uint32_t m = __float_as_uint(p) & 0x7FFFFFFFu;
+    return m < 0x00800000u || (m == 0x7F800000u && fmaxf(fabsf(a), fabsf(b)) < INFINITY);
 }
 
 // Nonzero if one of 16 e4m3 values is.
@@ -388,10 +391,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                     break;
                 }
                 float s1 = a0 * w0, s3 = a0 * w30;
-                // such blocks are added below, after the others
-                left |= beyond_f32(s1) || (EPI == EPI_SWIGLU && beyond_f32(s3));
-                s1 = beyond_f32(s1) ? 0.0f : s1;
-                s3 = beyond_f32(s3) ? 0.0f : s3;
+                if (__any_sync(0xffffffffu, not_normal(s1) || (EPI == EPI_SWIGLU && not_normal(s3)))) {
+                    // such blocks are added below, after the others
+                    const bool b1 = beyond_f32(s1, a0, w0), b3 = EPI == EPI_SWIGLU && beyond_f32(s3, a0, w30);
+                    s1 = b1 ? 0.0f : s1;
+                    s3 = b3 ? 0.0f : s3;
+                    left |= b1 || b3;
+                }
                 tc_fence_after();
                 if (active) {
                     const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
@@ -438,14 +444,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int kb = 0; kb < num_kb; ++kb) {
                     const int n = min(BK, g.K - kb * BK);
                     const float sa = __ldg(as + kb * g.rows);
-                    if (sa == 0.0f || !(beyond_f32(sa * __ldg(ws + kb)) || (EPI == EPI_SWIGLU && beyond_f32(sa * __ldg(ws3 + kb))))) continue;
+                    const auto beyond = [&](float sw) { return sa != 0.0f && sw != 0.0f && beyond_f32(sa * sw, sa, sw); };
+                    if (!beyond(__ldg(ws + kb)) && !(EPI == EPI_SWIGLU && beyond(__ldg(ws3 + kb)))) continue;
                     uint32_t any = 0;
                     for (int i = 0; i < n; i += 16) any |= nonzero16(a + kb * BK + i);
                     for (int j = 0; j < 128 && any != 0; ++j) {
                         const bool up = EPI == EPI_SWIGLU && j >= 64;
                         const float sw = __ldg((up ? ws3 : ws) + kb);
                         const int col = n0 + (EPI == EPI_SWIGLU ? half * 64 + (j & 63) : half * 128 + j);
-                        if (!beyond_f32(sa * sw) || sw == 0.0f || col >= g.n_out) continue;
+                        if (!beyond(sw) || col >= g.n_out) continue;
                         const uint8_t *w = (up ? g.w3 : g.w) + (static_cast<int64_t>(ti.e) * g.n_out + col) * g.K;
                         const float v = static_cast<float>(dot_e4m3(a + kb * BK, w + kb * BK, n) * (static_cast<double>(sa) * sw));
 #pragma unroll

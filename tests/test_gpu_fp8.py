@@ -230,6 +230,21 @@ def test_a_block_scale_of_zero_is_a_block_of_zeros():
     checked(M.moe_expert_matmul_fp8(a, off, w, out_dtype=F32, any_scales=True), want, bound)
 
 
+def test_an_infinite_scale_is_not_passed_over():
+    """Values times infinity are infinite or NaN, zeros NaN: never an ordinary number."""
+    a, w, off = _operands([40, 100], 272, 400, seed=34, free_scales=True)
+    clean = M.moe_expert_matmul_fp8(a, off, w, out_dtype=F32, any_scales=True)
+    a[0].view(torch.uint8)[7] = 0                      # rows of zeros, with an infinite scale and with the quantiser's
+    a[0].view(torch.uint8)[9] = 0
+    a[1][:, 9] = 2.0 ** -126
+    a[1][1, 7], a[1][2, 50] = float("inf"), -float("inf")
+    y = M.moe_expert_matmul_fp8(a, off, w, out_dtype=F32, any_scales=True)
+    assert torch.isnan(y[7]).all() and not torch.isfinite(y[50]).any() and not y[9].any()
+    keep = torch.ones(140, dtype=torch.bool, device=DEV)
+    keep[[7, 9, 50]] = False
+    assert torch.equal(y[keep], clean[keep])
+
+
 def test_scales_that_are_no_powers_of_two_are_reported():
     a, w, off = _operands([20, 30], 64, 272, seed=5)
     for scales, at in ((a[1], (1, 45)), (w[1], (1, 0, 2))):
